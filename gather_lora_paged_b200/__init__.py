@@ -23,6 +23,7 @@ SLORA_PAGEIN_KERNEL, SLORA_PAGEIN_MEMCPY = 0, 1
 SLORA_DECODE_AUTO, SLORA_DECODE_SPLIT, SLORA_DECODE_FUSED, SLORA_DECODE_STREAM = 0, 1, 2, 3
 SLORA_KIND_NONE, SLORA_KIND_TOKEN, SLORA_KIND_STREAM, SLORA_KIND_FUSED, SLORA_KIND_SPLIT = 0, 1, 2, 3, 4
 SLORA_WEIGHTS_16, SLORA_WEIGHTS_E4M3 = 0, 1
+SLORA_KV_16, SLORA_KV_E4M3 = 0, 1
 MAX_PROJ = 8
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "OOM", 3: "NOT_RESIDENT", 4: "CUDA", 5: "TIMEOUT",
@@ -49,6 +50,11 @@ class PoolStats(ctypes.Structure):
     _fields_ = [(n, c_int64) for n in ("page_ins", "hits", "evictions", "bytes_paged_in",
                                        "free_pages", "resident", "copy_calls", "epoch",
                                        "prefetched", "bytes_prefetched", "kv_pages")]
+
+
+class KvLayout(ctypes.Structure):
+    _fields_ = [("format", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+                ("reserved", c_int32 * 5)]
 
 
 _lib = None
@@ -79,6 +85,13 @@ def lib():
         "slora_quantize_e4m3_rows": ([I32, P, I64, I64, P, P], I32),
         "slora_kv_alloc": ([P, I64, P, P, P], I32),
         "slora_kv_free": ([P, P, I64, P], I32),
+        "slora_kv_page_tokens": ([P, POINTER(KvLayout)], I32),
+        "slora_kv_check_batch": ([P, POINTER(KvLayout), P, P, P, I64, I32, I32], I32),
+        "slora_kv_write": ([P, POINTER(KvLayout), P, I64, P, I64, P, P, P, I64, I32, I32, P], I32),
+        "slora_kv_read": ([P, POINTER(KvLayout), P, I64, P, I64, P, P, P, I64, I32, I32, P], I32),
+        "slora_kv_attention": ([P, POINTER(KvLayout), I32, P, I64, P, I64, P, P, P, P, I64, I32, I32, I32,
+                                c_float, I32, P, c_size_t, P], I32),
+        "slora_kv_attention_workspace_bytes": ([P, POINTER(KvLayout), I32, I32, I32, I32], c_size_t),
         "slora_adapter_evict": ([P, I32, P], I32),
         "slora_adapter_is_resident": ([P, I32, POINTER(c_int32)], I32),
         "slora_check_batch": ([P, P, I32], I32),
@@ -256,6 +269,58 @@ def slora_kv_alloc(pool: int, n: int, stream=None, done_event=None) -> list:
 def slora_kv_free(pool: int, ids, stream=None) -> None:
     a = _arr(c_int32, [int(i) for i in ids])
     _check(pool, lib().slora_kv_free(pool, ctypes.cast(a, c_void_p), len(ids), _stream(stream)))
+
+
+def make_kv_layout(n_kv_heads: int, head_dim: int, format: int = SLORA_KV_16) -> KvLayout:
+    """How one layer's K and V rows lie in KV pages (slora_kv_layout_t)."""
+    d = KvLayout()
+    d.format = format
+    d.n_kv_heads = n_kv_heads
+    d.head_dim = head_dim
+    return d
+
+
+def slora_kv_page_tokens(pool: int, layout: KvLayout) -> int:
+    return int(lib().slora_kv_page_tokens(pool, layout))
+
+
+def slora_kv_check_batch(pool: int, layout: KvLayout, row_start, kv_len, blocks, T: int) -> None:
+    """Host arrays: row_start (B + 1), kv_len (B), blocks (B x ldb)."""
+    import numpy as np
+    rs, kl = np.ascontiguousarray(row_start, np.int32), np.ascontiguousarray(kv_len, np.int32)
+    bl = np.ascontiguousarray(blocks, np.int32)
+    if rs.ndim != 1 or kl.ndim != 1 or bl.ndim != 2 or rs.size != kl.size + 1 or bl.shape[0] != kl.size:
+        raise ValueError("row_start (B + 1), kv_len (B) and blocks (B x ldb) do not fit together")
+    _check(pool, lib().slora_kv_check_batch(pool, layout, rs.ctypes.data, kl.ctypes.data, bl.ctypes.data,
+                                            bl.shape[1], kl.size, int(T)))
+
+
+def slora_kv_write(pool: int, layout: KvLayout, k, ldk: int, v, ldv: int, row_start, kv_len, blocks, ldb: int,
+                   B: int, T: int, stream=None) -> None:
+    _check(pool, lib().slora_kv_write(pool, layout, _ptr(k), ldk, _ptr(v), ldv, _ptr(row_start), _ptr(kv_len),
+                                      _ptr(blocks), ldb, B, T, _stream(stream)))
+
+
+def slora_kv_read(pool: int, layout: KvLayout, k, ldk: int, v, ldv: int, row_start, kv_len, blocks, ldb: int,
+                  B: int, T: int, stream=None) -> None:
+    _check(pool, lib().slora_kv_read(pool, layout, _ptr(k), ldk, _ptr(v), ldv, _ptr(row_start), _ptr(kv_len),
+                                     _ptr(blocks), ldb, B, T, _stream(stream)))
+
+
+def slora_kv_attention(pool: int, layout: KvLayout, n_q_heads: int, q, ldq: int, out, ldo: int, lse, row_start,
+                       kv_len, blocks, ldb: int, B: int, T: int, max_rows: int, scale: float, window: int,
+                       workspace, stream=None) -> None:
+    """lse: a float32 tensor or None; workspace: a device tensor of at least
+    slora_kv_attention_workspace_bytes() bytes."""
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(pool, lib().slora_kv_attention(pool, layout, n_q_heads, _ptr(q), ldq, _ptr(out), ldo, _ptr(lse),
+                                          _ptr(row_start), _ptr(kv_len), _ptr(blocks), ldb, B, T, max_rows, scale,
+                                          window, _ptr(workspace), size, _stream(stream)))
+
+
+def slora_kv_attention_workspace_bytes(pool: int, layout: KvLayout, n_q_heads: int, B: int, T: int,
+                                       max_rows: int) -> int:
+    return int(lib().slora_kv_attention_workspace_bytes(pool, layout, n_q_heads, B, T, max_rows))
 
 
 def slora_adapter_evict(pool: int, id: int, stream=None) -> None:

@@ -1,0 +1,247 @@
+// kv_cache.cu -- writing new tokens' K and V rows into the KV pages, as they
+// are or quantised to e4m3, and reading pages back into dense rows.
+//
+// Quantisation of one row x (one token, one head, K or V; D values):
+//     scale = RN32(max|x| / 448), at least 2^-126; code_d = e4m3(x_d / scale)
+// with the exact quotient rounded to nearest, ties to the even code.  An
+// all-zero row has scale 0; a row with an infinity or a NaN has scale NaN and
+// zero codes, so it reads back as NaN.  Reading: RN16(scale * value(code)).
+//
+// Both kernels move each byte once and are bound by HBM (small calls: by one
+// launch and a chain of three dependent loads).  A warp takes one token's
+// share of the work: kIter * 32 / (D / 8) rows of 8 values per lane, the
+// loads of all of them issued before the token's page is looked up, so that the
+// look-up's latency hides behind them.
+#include "kv_common.cuh"
+
+namespace slora {
+namespace {
+
+constexpr int kWarps = 8;   // per CTA
+constexpr int kIter = 4;    // 16-byte loads in flight per lane
+
+// The sequence of row t and its position (the whole warp asks for one t): a
+// 32-way search of row_start, after a look at sequence t itself, which is the
+// answer when every sequence has one row.  False: no usable sequence owns t, or
+// its position lies before the cache's first token.
+__device__ __forceinline__ bool kv_locate(const KvDev& P, int t, int& b, int& pos) {
+  KvSeq s;
+  const int lane = threadIdx.x & 31;
+  b = t;
+  if (!(t < P.B && __ldg(P.row_start + t) <= t && t < __ldg(P.row_start + t + 1))) {
+    int lo = 0, cnt = P.B + 1;  // the last of [lo, lo + cnt) with row_start <= t
+    while (cnt > 1) {
+      const int step = (cnt + 31) >> 5;
+      const bool in = lane * step < cnt && __ldg(P.row_start + lo + lane * step) <= t;
+      const unsigned m = __ballot_sync(FULL_MASK, in);
+      if (!m) return false;
+      const int k = 31 - __clz(m);
+      lo += k * step;
+      cnt = min(step, cnt - k * step);
+    }
+    b = lo;
+    if (b >= P.B) return false;
+  }
+  if (!kv_seq(P, b, INT32_MAX, s) || t < s.row0 || t >= s.row0 + s.n) return false;
+  pos = s.len - s.n + (t - s.row0);
+  return pos >= 0;
+}
+
+// |value| of an e4m3 code.
+__device__ __forceinline__ float e4m3_abs(uint32_t code) {
+  const uint32_t h = e4m3x2_f16x2(code & 0x7f);
+  return __low2float(*reinterpret_cast<const __half2*>(&h));
+}
+
+// e4m3 code of the exact quotient x / scale, given rinv = RN(1 / scale).  The
+// product x * rinv is within 2^-22 of the quotient, so where its two neighbours
+// at that distance have one code, that is the code; where they do not, the
+// border m between their (adjacent) codes is compared with x exactly: m has 5
+// significant bits and scale 24, so m * scale is exact in 64 bits.
+__device__ __forceinline__ uint32_t e4m3_settle(float ax, float scale, uint32_t lo, uint32_t hi) {
+  const double m = 0.5 * ((double)e4m3_abs(lo) + (double)e4m3_abs(hi)) * (double)scale;
+  if ((double)ax > m) return hi;
+  if ((double)ax < m) return lo;
+  return (lo & 1) ? hi : lo;
+}
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {  // a in the low byte
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t quantise4(const float* f, float scale, float rinv) {
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float a = f[2 * i] * rinv, b = f[2 * i + 1] * rinv;
+    lo |= cvt_e4m3x2(a * (1.0f - 0x1p-22f), b * (1.0f - 0x1p-22f)) << (16 * i);
+    hi |= cvt_e4m3x2(a * (1.0f + 0x1p-22f), b * (1.0f + 0x1p-22f)) << (16 * i);
+  }
+  if (lo != hi) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t l = (lo >> (8 * i)) & 0xff, h = (hi >> (8 * i)) & 0xff;
+      if (l != h) {
+        const uint32_t c = e4m3_settle(fabsf(f[i]), scale, l & 0x7f, h & 0x7f) | (l & 0x80);
+        lo = (lo & ~(0xffu << (8 * i))) | (c << (8 * i));
+      }
+    }
+  }
+  return lo;
+}
+
+// Units: (token, block of kIter * RPI of its 2 * H rows); a warp per unit.
+template <int DT, int FMT, int D>
+__global__ void __launch_bounds__(kWarps * 32) k_kv_write(KvDev P, const uint16_t* k, int64_t ldk, const uint16_t* v,
+                                                          int64_t ldv, int per_token) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per pass
+  const int lane = threadIdx.x & 31, col = (lane % LPR) * 8;
+  if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX);
+  const int units = P.T * per_token;
+  for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
+    const int t = u / per_token, r0 = (u - t * per_token) * (kIter * RPI) + lane / LPR;
+    uint4 x[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int r = r0 + i * RPI;
+      if (r < 2 * P.H) {
+        const uint16_t* src = r < P.H ? k + (int64_t)t * ldk + (int64_t)r * D : v + (int64_t)t * ldv + (int64_t)(r - P.H) * D;
+        x[i] = __ldg(reinterpret_cast<const uint4*>(src + col));
+      } else {
+        x[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    int b, pos;
+    if (!kv_locate(P, t, b, pos)) continue;
+    const uint32_t row = kv_row(P, b, pos, 0);
+    if (row == kNoRow) continue;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int r = r0 + i * RPI;
+      const uint32_t dst = row + (uint32_t)(r * P.pt);  // row r = (part, head)
+      if (FMT == SLORA_KV_16) {
+        if (r < 2 * P.H) *reinterpret_cast<uint4*>(P.pool + (int64_t)dst * D + col) = x[i];
+      } else {
+        float f[8];
+        unpack8<DT>(x[i], f);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+        float scale = 0.f;
+        uint2 codes = make_uint2(0, 0);
+        if (top >= 0x7f800000u) {
+          scale = __uint_as_float(0x7fc00000u);
+        } else if (top) {
+          scale = fmaxf(__fdiv_rn(__uint_as_float(top), 448.f), 0x1p-126f);
+          const float rinv = __frcp_rn(scale);
+          codes = make_uint2(quantise4(f, scale, rinv), quantise4(f + 4, scale, rinv));
+        }
+        if (r < 2 * P.H) {
+          *reinterpret_cast<uint2*>(reinterpret_cast<unsigned char*>(P.pool) + (int64_t)dst * D + col) = codes;
+          if (col == 0) *kv_scale(P, dst) = scale;
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int FMT, int D>
+__global__ void __launch_bounds__(kWarps * 32) k_kv_read(KvDev P, uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv,
+                                                         int per_token) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR;
+  const int lane = threadIdx.x & 31, col = (lane % LPR) * 8;
+  if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX);
+  const int units = P.T * per_token;
+  for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
+    const int t = u / per_token, r0 = (u - t * per_token) * (kIter * RPI) + lane / LPR;
+    int b, pos;
+    if (!kv_locate(P, t, b, pos)) continue;
+    const uint32_t row = kv_row(P, b, pos, 0);
+    if (row == kNoRow) continue;
+    uint4 x[kIter];
+    float scale[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int r = r0 + i * RPI;
+      const uint32_t src = row + (uint32_t)(r * P.pt);
+      x[i] = make_uint4(0, 0, 0, 0);
+      scale[i] = 0.f;
+      if (r < 2 * P.H) {
+        if (FMT == SLORA_KV_16) {
+          x[i] = *reinterpret_cast<const uint4*>(P.pool + (int64_t)src * D + col);
+        } else {
+          const uint2 c = *reinterpret_cast<const uint2*>(reinterpret_cast<const unsigned char*>(P.pool) +
+                                                          (int64_t)src * D + col);
+          x[i].x = c.x;
+          x[i].y = c.y;
+          scale[i] = *kv_scale(P, src);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int r = r0 + i * RPI;
+      if (r >= 2 * P.H) break;
+      if (FMT == SLORA_KV_E4M3) {
+        const uint32_t w[2] = {x[i].x, x[i].y};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t h = e4m3x2_f16x2(w[j >> 1] >> (16 * (j & 1)));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          o[j] = pack2<DT>(f.x * scale[i], f.y * scale[i]);
+        }
+        x[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      uint16_t* dst = r < P.H ? k + (int64_t)t * ldk + (int64_t)r * D : v + (int64_t)t * ldv + (int64_t)(r - P.H) * D;
+      *reinterpret_cast<uint4*>(dst + col) = x[i];
+    }
+  }
+}
+
+struct Grid {
+  int grid, per_token;
+};
+Grid grid_for(const KvDev& P, int D, int sm_count) {
+  const int rows = kIter * 32 / (D / 8);
+  Grid g;
+  g.per_token = cdiv_i(2 * P.H, rows);
+  const int64_t ctas = ((int64_t)P.T * g.per_token + kWarps - 1) / kWarps;
+  g.grid = (int)(ctas < (int64_t)sm_count * 8 ? ctas : (int64_t)sm_count * 8);
+  return g;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvDev& P, int dtype, int fmt, int D, const void* k, int64_t ldk, const void* v,
+                            int64_t ldv, int sm_count, cudaStream_t s) {
+  const Grid g = grid_for(P, D, sm_count);
+  auto go = [&](auto kern) {
+    kern<<<g.grid, kWarps * 32, 0, s>>>(P, static_cast<const uint16_t*>(k), ldk, static_cast<const uint16_t*>(v), ldv,
+                                        g.per_token);
+    return cudaGetLastError();
+  };
+  if (fmt == SLORA_KV_16)  // a copy: the element type does not matter
+    return D == 64 ? go(k_kv_write<SLORA_F16, SLORA_KV_16, 64>) : go(k_kv_write<SLORA_F16, SLORA_KV_16, 128>);
+  if (dtype == SLORA_F16)
+    return D == 64 ? go(k_kv_write<SLORA_F16, SLORA_KV_E4M3, 64>) : go(k_kv_write<SLORA_F16, SLORA_KV_E4M3, 128>);
+  return D == 64 ? go(k_kv_write<SLORA_BF16, SLORA_KV_E4M3, 64>) : go(k_kv_write<SLORA_BF16, SLORA_KV_E4M3, 128>);
+}
+
+cudaError_t launch_kv_read(const KvDev& P, int dtype, int fmt, int D, void* k, int64_t ldk, void* v, int64_t ldv,
+                           int sm_count, cudaStream_t s) {
+  const Grid g = grid_for(P, D, sm_count);
+  auto go = [&](auto kern) {
+    kern<<<g.grid, kWarps * 32, 0, s>>>(P, static_cast<uint16_t*>(k), ldk, static_cast<uint16_t*>(v), ldv, g.per_token);
+    return cudaGetLastError();
+  };
+  if (fmt == SLORA_KV_16)
+    return D == 64 ? go(k_kv_read<SLORA_F16, SLORA_KV_16, 64>) : go(k_kv_read<SLORA_F16, SLORA_KV_16, 128>);
+  if (dtype == SLORA_F16)
+    return D == 64 ? go(k_kv_read<SLORA_F16, SLORA_KV_E4M3, 64>) : go(k_kv_read<SLORA_F16, SLORA_KV_E4M3, 128>);
+  return D == 64 ? go(k_kv_read<SLORA_BF16, SLORA_KV_E4M3, 64>) : go(k_kv_read<SLORA_BF16, SLORA_KV_E4M3, 128>);
+}
+
+}  // namespace slora

@@ -224,6 +224,7 @@ struct slora_pool {
   int64_t n_rel = 0;                  // release events recorded so far
   PoolDev pd{};
   int sm_count = 148;
+  int device = -1;                    // the device the pool was created on
   int grid_shrink = 0, grid_expand = 0, grid_stream = 0;
   int inject_after = -1;
   cudaEvent_t phase_ev[8] = {};
@@ -610,6 +611,7 @@ slora_status_t slora_pool_create(const slora_pool_desc* desc, slora_pool** out) 
     cudaError_t e = cudaSuccess;
     int dev = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    P->device = dev;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->sm_count, cudaDevAttrMultiProcessorCount, dev);
     for (int i = 0; i < kEventRing && e == cudaSuccess; ++i)
       e = cudaEventCreateWithFlags(&P->ev[i], cudaEventDisableTiming);
@@ -1124,6 +1126,191 @@ slora_status_t slora_kv_free(slora_pool* P, const int32_t* ids, int64_t n, void*
   }
   P->kv_held -= n;
   P->st.free_pages = (int64_t)P->free_pages.size();
+  return SLORA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// KV cache: write, read back, attention over the pool's pages.
+
+static bool kv_layout_ok(const slora_kv_layout_t* L) {
+  return L && (L->format == SLORA_KV_16 || L->format == SLORA_KV_E4M3) && L->n_kv_heads >= 1 && L->n_kv_heads <= 256 &&
+         (L->head_dim == 64 || L->head_dim == 128);
+}
+
+static int64_t kv_page_tokens_of(const slora_pool* P, const slora_kv_layout_t* L) {
+  const int64_t row = L->format == SLORA_KV_E4M3 ? L->head_dim + 4 : 2 * L->head_dim;  // bytes, scale included
+  return 2 * P->d.page_elems / (2 * L->n_kv_heads * row);
+}
+
+int32_t slora_kv_page_tokens(const slora_pool* P, const slora_kv_layout_t* layout) {
+  if (!P || !kv_layout_ok(layout)) return 0;
+  return (int32_t)std::min<int64_t>(kv_page_tokens_of(P, layout), INT32_MAX);
+}
+
+// The checks that all KV calls share; fills the kernels' view of the batch.
+static slora_status_t kv_plan(slora_pool* P, const slora_kv_layout_t* L, const int32_t* row_start, const int32_t* kv_len,
+                              const int32_t* blocks, int64_t ldb, int32_t B, int32_t T, KvDev& K) {
+  if (!L) return P->fail(SLORA_ERR_INVALID_ARG, "layout is NULL");
+  if (L->format != SLORA_KV_16 && L->format != SLORA_KV_E4M3) return P->fail(SLORA_ERR_INVALID_ARG, "layout format");
+  if (L->n_kv_heads < 1 || L->n_kv_heads > 256) return P->fail(SLORA_ERR_INVALID_ARG, "n_kv_heads out of [1, 256]");
+  if (L->head_dim != 64 && L->head_dim != 128)
+    return P->fail(SLORA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  const int64_t pt = kv_page_tokens_of(P, L);
+  if (pt < 1) return P->fail(SLORA_ERR_INVALID_ARG, "a page does not hold one token of this layout");
+  if (B < 0 || T < 0 || T > P->d.max_tokens) return P->fail(SLORA_ERR_INVALID_ARG, "B negative or T out of [0, max_tokens]");
+  if (B > 0 && (!row_start || !kv_len)) return P->fail(SLORA_ERR_INVALID_ARG, "row_start or kv_len is NULL");
+  if (ldb < 0 || (B > 0 && ldb > 0 && !blocks)) return P->fail(SLORA_ERR_INVALID_ARG, "blocks is NULL or ldb negative");
+  if (((uintptr_t)row_start | (uintptr_t)kv_len | (uintptr_t)blocks) % 4)
+    return P->fail(SLORA_ERR_INVALID_ARG, "row_start, kv_len and blocks must be 4-byte aligned");
+  K = KvDev{};
+  K.pool = static_cast<uint16_t*>(P->d.dev_pool);
+  int sh = 0;
+  while ((1ll << sh) < P->d.page_elems) ++sh;
+  K.page_shift = sh;
+  K.row_shift = sh + (L->format == SLORA_KV_E4M3 ? 1 : 0) - (L->head_dim == 64 ? 6 : 7);
+  if ((P->d.n_pages << K.row_shift) >= (int64_t)UINT32_MAX)
+    return P->fail(SLORA_ERR_UNSUPPORTED, "the pool holds 2^32 rows of head_dim values or more");
+  K.n_pages = (int)P->d.n_pages;
+  K.H = L->n_kv_heads;
+  K.pt = (int)pt;
+  K.scale_off = (int)(2 * (int64_t)L->n_kv_heads * pt * L->head_dim / 4);
+  K.row_start = row_start;
+  K.kv_len = kv_len;
+  K.blocks = blocks;
+  K.ldb = ldb;
+  const int64_t most = 1ll << 30;  // tokens of one sequence
+  K.capacity = ldb > most / pt ? most : ldb * pt;
+  K.B = B;
+  K.T = T;
+  return SLORA_OK;
+}
+
+// The device part of the checks, once the arguments are known to be right.
+static slora_status_t kv_device(slora_pool* P, KvDev& K) {
+  slora_status_t s = need_device(P);
+  if (s) return s;
+  int dev = -1;
+  CUDA_TRY(P, cudaGetDevice(&dev));
+  if (dev != P->device)
+    return P->fail(SLORA_ERR_INVALID_ARG, "the current device is not the one the pool was created on");
+  K.err = P->pd.err;
+  return SLORA_OK;
+}
+
+static slora_status_t kv_rows(slora_pool* P, const char* name, const void* x, int64_t ld, int64_t width) {
+  if (!x) return P->fail(SLORA_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (ld < width || ld % 8 || !aligned16(x))
+    return P->fail(SLORA_ERR_INVALID_ARG,
+                   std::string(name) + " must be 16-byte aligned with a leading dimension >= heads * head_dim, a multiple of 8");
+  return SLORA_OK;
+}
+
+slora_status_t slora_kv_check_batch(const slora_pool* Pc, const slora_kv_layout_t* layout, const int32_t* row_start,
+                                    const int32_t* kv_len, const int32_t* blocks, int64_t ldb, int32_t B, int32_t T) {
+  slora_pool* P = const_cast<slora_pool*>(Pc);
+  if (!P) return SLORA_ERR_INVALID_ARG;
+  KvDev K;
+  slora_status_t s = kv_plan(P, layout, row_start, kv_len, blocks, ldb, B, T, K);
+  if (s) return s;
+  for (int32_t b = 0; b < B; ++b) {
+    const std::string who = "sequence " + std::to_string(b);
+    if (row_start[b] < 0 || row_start[b + 1] < row_start[b] || row_start[b + 1] > T)
+      return P->fail(SLORA_ERR_INVALID_ARG, who + ": rows outside [0, T] or not ascending");
+    if (kv_len[b] < 0 || kv_len[b] > K.capacity)
+      return P->fail(SLORA_ERR_INVALID_ARG, who + ": kv_len outside [0, ldb * page_tokens]");
+    for (int64_t i = 0; i < cdiv64(kv_len[b], K.pt); ++i) {
+      const int32_t pg = blocks[(int64_t)b * ldb + i];
+      if (pg < 0 || pg >= P->d.n_pages || !P->kv_page[pg])
+        return P->fail(SLORA_ERR_INVALID_ARG, who + ": page " + std::to_string(pg) + " is not a held KV page");
+    }
+  }
+  return SLORA_OK;
+}
+
+slora_status_t slora_kv_write(slora_pool* P, const slora_kv_layout_t* layout, const void* k, int64_t ldk, const void* v,
+                              int64_t ldv, const int32_t* row_start, const int32_t* kv_len, const int32_t* blocks,
+                              int64_t ldb, int32_t B, int32_t T, void* stream) {
+  NvtxRange nvtx_("slora_kv_write");
+  if (!P) return SLORA_ERR_INVALID_ARG;
+  KvDev K;
+  slora_status_t s = kv_plan(P, layout, row_start, kv_len, blocks, ldb, B, T, K);
+  if (s) return s;
+  const int64_t width = (int64_t)layout->n_kv_heads * layout->head_dim;
+  if (T > 0 && ((s = kv_rows(P, "k", k, ldk, width)) || (s = kv_rows(P, "v", v, ldv, width)))) return s;
+  if ((s = kv_device(P, K))) return s;
+  if (T == 0 || B == 0) return SLORA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  phase(P, 0, 1, st);
+  CUDA_TRY(P, launch_kv_write(K, P->d.dtype, layout->format, layout->head_dim, k, ldk, v, ldv, P->sm_count, st));
+  phase(P, 1, 1, st);
+  return SLORA_OK;
+}
+
+slora_status_t slora_kv_read(slora_pool* P, const slora_kv_layout_t* layout, void* k, int64_t ldk, void* v, int64_t ldv,
+                             const int32_t* row_start, const int32_t* kv_len, const int32_t* blocks, int64_t ldb,
+                             int32_t B, int32_t T, void* stream) {
+  NvtxRange nvtx_("slora_kv_read");
+  if (!P) return SLORA_ERR_INVALID_ARG;
+  KvDev K;
+  slora_status_t s = kv_plan(P, layout, row_start, kv_len, blocks, ldb, B, T, K);
+  if (s) return s;
+  const int64_t width = (int64_t)layout->n_kv_heads * layout->head_dim;
+  if (T > 0 && ((s = kv_rows(P, "k", k, ldk, width)) || (s = kv_rows(P, "v", v, ldv, width)))) return s;
+  if ((s = kv_device(P, K))) return s;
+  if (T == 0 || B == 0) return SLORA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  phase(P, 0, 1, st);
+  CUDA_TRY(P, launch_kv_read(K, P->d.dtype, layout->format, layout->head_dim, k, ldk, v, ldv, P->sm_count, st));
+  phase(P, 1, 1, st);
+  return SLORA_OK;
+}
+
+size_t slora_kv_attention_workspace_bytes(const slora_pool* P, const slora_kv_layout_t* layout, int32_t n_q_heads,
+                                          int32_t B, int32_t T, int32_t max_rows) {
+  if (!P || !kv_layout_ok(layout) || n_q_heads < 1 || n_q_heads % layout->n_kv_heads || B < 1 || T < 1 || max_rows < 1)
+    return 0;
+  return kv_attention_workspace(layout->head_dim, n_q_heads / layout->n_kv_heads, std::min(max_rows, T), P->sm_count);
+}
+
+slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout, int32_t n_q_heads, const void* q,
+                                  int64_t ldq, void* out, int64_t ldo, float* lse, const int32_t* row_start,
+                                  const int32_t* kv_len, const int32_t* blocks, int64_t ldb, int32_t B, int32_t T,
+                                  int32_t max_rows, float scale, int32_t window, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  NvtxRange nvtx_("slora_kv_attention");
+  if (!P) return SLORA_ERR_INVALID_ARG;
+  KvAttnDev A{};
+  slora_status_t s = kv_plan(P, layout, row_start, kv_len, blocks, ldb, B, T, A.kv);
+  if (s) return s;
+  if (n_q_heads < 1 || n_q_heads > 1024 || n_q_heads % layout->n_kv_heads)
+    return P->fail(SLORA_ERR_INVALID_ARG, "n_q_heads must be a multiple of n_kv_heads in [1, 1024]");
+  if (max_rows < 1 && B > 0 && T > 0) return P->fail(SLORA_ERR_INVALID_ARG, "max_rows must be positive");
+  if (!std::isfinite(scale) || scale <= 0.f) return P->fail(SLORA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (window < 0) return P->fail(SLORA_ERR_INVALID_ARG, "window is negative (0: none)");
+  const int64_t width = (int64_t)n_q_heads * layout->head_dim;
+  if (T > 0 && ((s = kv_rows(P, "q", q, ldq, width)) || (s = kv_rows(P, "out", out, ldo, width)))) return s;
+  if (T > 0 && q == out) return P->fail(SLORA_ERR_INVALID_ARG, "out must not overlap q");
+  if ((uintptr_t)lse % 4) return P->fail(SLORA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  const size_t need = slora_kv_attention_workspace_bytes(P, layout, n_q_heads, B, T, max_rows);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return P->fail(SLORA_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold " + std::to_string(need) + " bytes");
+  if ((s = kv_device(P, A.kv))) return s;
+  if (T == 0 || B == 0) return SLORA_OK;
+  A.q = static_cast<const uint16_t*>(q);
+  A.ldq = ldq;
+  A.out = static_cast<uint16_t*>(out);
+  A.ldo = ldo;
+  A.lse = lse;
+  A.Hq = n_q_heads;
+  A.G = n_q_heads / layout->n_kv_heads;
+  A.c = (float)((double)scale * 1.4426950408889634);
+  A.window = window;
+  A.max_rows = std::min(max_rows, T);
+  A.workspace = workspace;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  phase(P, 0, 1, st);
+  CUDA_TRY(P, launch_kv_attention(A, P->d.dtype, layout->format, layout->head_dim, P->sm_count, st));
+  phase(P, 1, 1, st);
   return SLORA_OK;
 }
 

@@ -155,4 +155,42 @@ cudaError_t launch_gather_debug(const PoolDev& pool, int id, int d, int list_off
                                 uint16_t* out_dev, cudaStream_t s);
 int occupancy_blocks(int which);   // resident CTAs per SM of the decode kernels
 
+// ---------------------------------------------------------------------------
+// KV cache in the pool's pages (kv_common.cuh has the page layout).
+struct KvDev {
+  uint16_t* pool;
+  int page_shift;            // log2(page_elems)
+  int row_shift;             // log2(rows of head_dim values per page)
+  int n_pages;
+  int H;                     // kv heads
+  int pt;                    // tokens per page
+  int scale_off;             // e4m3: floats from a page's start to its scales
+  const int32_t* row_start;  // [B + 1]
+  const int32_t* kv_len;     // [B]
+  const int32_t* blocks;     // [B][ldb]
+  int64_t ldb;
+  int64_t capacity;          // tokens a table row can name: ldb * pt
+  int B, T;
+  int32_t* err;
+};
+struct KvAttnDev {
+  KvDev kv;
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* out;
+  int64_t ldo;
+  float* lse;                // [T][Hq], may be NULL
+  int Hq, G;                 // query heads, query heads per kv head
+  float c;                   // scale * log2(e)
+  int window;                // 0: none
+  int max_rows;
+  void* workspace;
+};
+cudaError_t launch_kv_write(const KvDev& P, int dtype, int fmt, int D, const void* k, int64_t ldk, const void* v,
+                            int64_t ldv, int sm_count, cudaStream_t s);
+cudaError_t launch_kv_read(const KvDev& P, int dtype, int fmt, int D, void* k, int64_t ldk, void* v, int64_t ldv,
+                           int sm_count, cudaStream_t s);
+cudaError_t launch_kv_attention(const KvAttnDev& A, int dtype, int fmt, int D, int sm_count, cudaStream_t s);
+size_t kv_attention_workspace(int D, int G, int max_rows, int sm_count);
+
 }  // namespace slora

@@ -321,6 +321,108 @@ slora_status_t slora_kv_alloc(slora_pool* pool, int64_t n, int32_t* ids_out, voi
  * changed), TIMEOUT, CUDA.                                                    */
 slora_status_t slora_kv_free(slora_pool* pool, const int32_t* ids, int64_t n, void* stream);
 
+/* ---- the KV cache in the pool's pages: write, read back, attend ------------- */
+
+/* How KV pages store K and V rows (one row: one token, one kv head, K or V). */
+typedef enum {
+  SLORA_KV_16 = 0,             /* the pool's 16-bit dtype                           */
+  SLORA_KV_E4M3 = 1            /* e4m3 codes with one fp32 scale per row: value =
+                                  scale * value(code).  About half the pages and half
+                                  the bytes that attention reads                    */
+} slora_kv_format_t;
+
+/* One layer's KV cache over pages lent by slora_kv_alloc.  A page holds
+ * slora_kv_page_tokens() tokens: rows [K, V][n_kv_heads][token][head_dim], and
+ * in e4m3 then the row scales [K, V][n_kv_heads][token].  Any number of
+ * layouts may share a pool (each on its own pages), whatever its weight_format. */
+typedef struct {
+  int32_t format;       /* slora_kv_format_t                                       */
+  int32_t n_kv_heads;   /* 1..256 (of this rank's shard, say)                      */
+  int32_t head_dim;     /* 64 or 128                                               */
+  int32_t reserved[5];
+} slora_kv_layout_t;
+
+/* Tokens one page holds: floor(page bytes / bytes of a token's 2 * n_kv_heads
+ * rows, scales included); need not be a power of two.  0: not one, or a bad
+ * argument.  Host only.                                                       */
+int32_t slora_kv_page_tokens(const slora_pool* pool, const slora_kv_layout_t* layout);
+
+/* The batch that the calls below share (all arrays device int32):
+ *   - row_start[B + 1], ascending: sequence b owns rows [row_start[b],
+ *     row_start[b + 1]) of the T-row tensors of the call, its newest n tokens in
+ *     order; rows of no sequence (behind the last one, say) are left as they are;
+ *   - kv_len[B]: tokens of sequence b up to and including these rows, at most
+ *     ldb * page_tokens and 2^30.  Row i of its n rows has position
+ *     kv_len[b] - n + i; a row with a negative position has no place in the cache
+ *     (not written, not read, and its attention sees no key);
+ *   - blocks[B][ldb]: blocks[b][p / page_tokens] is the page of position p.
+ * So one step's three arrays serve the write of its new tokens, their attention
+ * and, with kv_len[b] the end of a range, the reading of any range.  Checked on
+ * the device: a sequence whose rows or kv_len are out of range is skipped
+ * (code 8, info = sequence); a position whose page id lies outside the pool is
+ * not written or read, and attention leaves its key out (code 9, info =
+ * sequence).  Page ids are not checked against ownership on the device: that is
+ * slora_kv_check_batch.  Two sequences may share pages (a common prefix) as long
+ * as no call writes a position of a shared page twice.
+ * Tensors have T rows of heads * head_dim contiguous 16-bit elements (the pool's
+ * dtype), 16-byte aligned, leading dimensions in elements, multiples of 8.
+ * Nothing is allocated and dev_scratch is not used: the calls can be captured
+ * into CUDA graphs and run beside the pool's other calls.  The current device
+ * must be the one the pool was created on.
+ * Errors of all three: INVALID_ARG, UNSUPPORTED (head_dim; a pool of 2^32 rows
+ * of head_dim values), CUDA.                                                   */
+
+/* Host-side check of such a batch before its arrays are copied to the device
+ * (row_start, kv_len and blocks are HOST arrays here): ranges as above, and every
+ * page that a position below kv_len uses is held as a KV page.
+ * Errors: INVALID_ARG.                                                         */
+slora_status_t slora_kv_check_batch(const slora_pool* pool, const slora_kv_layout_t* layout, const int32_t* row_start,
+                                    const int32_t* kv_len, const int32_t* blocks, int64_t ldb, int32_t B, int32_t T);
+
+/* Writes the K and V rows of new tokens (k, v: T x n_kv_heads*head_dim) into
+ * their pages.  16-bit: the bits as they are.  e4m3, per row x: scale =
+ * max|x| / 448 in fp32 (at least 2^-126), code = the e4m3 value nearest to the
+ * exact x / scale, ties to the even code; an all-zero row has scale 0; a row
+ * with an infinity or a NaN has scale NaN and zero codes, and reads as NaN.  */
+slora_status_t slora_kv_write(slora_pool* pool, const slora_kv_layout_t* layout, const void* k, int64_t ldk,
+                              const void* v, int64_t ldv, const int32_t* row_start, const int32_t* kv_len,
+                              const int32_t* blocks, int64_t ldb, int32_t B, int32_t T, void* stream);
+
+/* Reads the K and V rows of the batch's positions back into dense k, v (T x
+ * n_kv_heads*head_dim): the bits of 16-bit rows; RN(scale * value(code)) of e4m3
+ * rows.  For export, migration and tests.                                      */
+slora_status_t slora_kv_read(slora_pool* pool, const slora_kv_layout_t* layout, void* k, int64_t ldk, void* v,
+                             int64_t ldv, const int32_t* row_start, const int32_t* kv_len, const int32_t* blocks,
+                             int64_t ldb, int32_t B, int32_t T, void* stream);
+
+/* Attention of each sequence's n newest tokens (one in decode, several drafted
+ * ones, a chunk of a prompt, mixed freely) over its cache, whose last n
+ * positions are those tokens' own, written before:
+ *     out[i, hq] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q[i, hq] . k_j)
+ * over the keys j of kv head hq / (n_q_heads / n_kv_heads) with j <= the row's
+ * position and, if window > 0, j > position - window; lse[i, hq] = log sum_j w_j
+ * (natural; T x n_q_heads fp32 contiguous; may be NULL).  A row that sees no key
+ * gets 0 and -inf.  Keys that a row does not see have no influence on it,
+ * whatever their bits.  q, out: T x n_q_heads*head_dim, not overlapping.  Sums and
+ * statistics are fp32, out is rounded once.
+ *   - max_rows: a host-side bound on the rows of any one sequence (longer ones
+ *     are skipped, code 8): 1 for a decode step, T where nothing is known;
+ *   - workspace: slora_kv_attention_workspace_bytes() bytes of device memory,
+ *     16-byte aligned, contents irrelevant before and after the call.  Calls that
+ *     may overlap on the GPU, replays of captured graphs among them, need
+ *     workspaces of their own.
+ * Results do not depend on timing: repeat calls are bit-identical.             */
+slora_status_t slora_kv_attention(slora_pool* pool, const slora_kv_layout_t* layout, int32_t n_q_heads, const void* q,
+                                  int64_t ldq, void* out, int64_t ldo, float* lse, const int32_t* row_start,
+                                  const int32_t* kv_len, const int32_t* blocks, int64_t ldb, int32_t B, int32_t T,
+                                  int32_t max_rows, float scale, int32_t window, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Workspace of slora_kv_attention for calls of up to B sequences, T rows and
+ * max_rows rows per sequence (0 for a bad argument).  Host only.              */
+size_t slora_kv_attention_workspace_bytes(const slora_pool* pool, const slora_kv_layout_t* layout, int32_t n_q_heads,
+                                          int32_t B, int32_t T, int32_t max_rows);
+
 /* Evicts one resident adapter now (its pages become free once the compute that
  * last used it has finished; the device table entry is cleared on `stream`). */
 slora_status_t slora_adapter_evict(slora_pool* pool, int32_t id, void* stream);
