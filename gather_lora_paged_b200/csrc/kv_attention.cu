@@ -44,7 +44,7 @@
 
 #include <atomic>
 
-#include "kv_common.cuh"
+#include "kv_attn.cuh"
 
 namespace slora {
 namespace {
@@ -54,7 +54,6 @@ constexpr int kTK = 64;       // keys per tile
 constexpr int kTM = 64;       // rows per row tile
 constexpr int kMinRun = 2;    // tiles that are worth a CTA of their own
 constexpr int kCtasPerSm = 2;
-constexpr float kLn2 = 0.69314718055994531f;
 
 template <int FMT, int D>
 struct Cfg {
@@ -69,94 +68,6 @@ struct Cfg {
   static constexpr int kOffStat = kOffMask + (kStages + 2) * 8;
   static constexpr int kSmem = kOffStat + 2 * 16 * 2 * 4;
   static_assert(kSmem <= (233472 / kCtasPerSm) - 1024 - 128, "two CTAs per SM");
-};
-
-// A split item, written by the CTA whose run holds its first tile.
-struct Split {
-  int b, h, rt, slot;  // the first partial; the others are the even slots of the next CTAs
-  int n;               // partials (0: none)
-  int pad[3];
-};
-
-__host__ __device__ inline size_t slot_floats(int D) { return (size_t)kTM * (D + 2); }
-
-struct Span {
-  int lo, hi;       // keys some row of the tile sees
-  int t0, t1;       // key tiles (at least one)
-};
-
-// Keys of rows [rt * kTM, ...) of a sequence.
-__device__ __forceinline__ Span span_of(const KvSeq& s, int G, int window, int rt) {
-  const int R = s.n * G, r0 = rt * kTM, r1 = min(R, r0 + kTM) - 1;
-  const int first = s.len - s.n;
-  Span x;
-  x.hi = max(0, first + r1 / G + 1);
-  x.lo = window > 0 ? max(0, first + r0 / G - window + 1) : 0;
-  x.t0 = x.lo / kTK;
-  x.t1 = max(x.t0 + 1, (x.hi + kTK - 1) / kTK);
-  return x;
-}
-__device__ __forceinline__ bool takes(const KvAttnDev& A, int row_limit, int b, KvSeq& s) {
-  return kv_seq(A.kv, b, A.max_rows, s) && s.n > 0 && (int64_t)s.n * A.G <= row_limit;
-}
-// Tiles of all items of sequence b.
-__device__ __forceinline__ long long seq_tiles(const KvAttnDev& A, int row_limit, int b) {
-  KvSeq s;
-  if (!takes(A, row_limit, b, s)) return 0;
-  const int RT = cdiv_i(s.n * A.G, kTM);
-  long long u = 0;
-  for (int rt = 0; rt < RT; ++rt) {
-    const Span x = span_of(s, A.G, A.window, rt);
-    u += x.t1 - x.t0;
-  }
-  return u * A.kv.H;
-}
-
-// A place in the line of tiles.
-struct Cursor {
-  KvSeq s;
-  Span x;
-  int b, h, rt, RT, tile;
-  long long left;  // tiles of this CTA from here on
-
-  __device__ void seek(const KvAttnDev& A, int row_limit, int b_, long long off) {
-    b = b_;
-    takes(A, row_limit, b, s);
-    RT = cdiv_i(s.n * A.G, kTM);
-    long long per = 0;
-    for (rt = 0; rt < RT; ++rt) {
-      x = span_of(s, A.G, A.window, rt);
-      per += x.t1 - x.t0;
-    }
-    h = (int)(off / per);
-    off -= h * per;
-    for (rt = 0;; ++rt) {
-      x = span_of(s, A.G, A.window, rt);
-      if (off < x.t1 - x.t0) break;
-      off -= x.t1 - x.t0;
-    }
-    tile = x.t0 + (int)off;
-  }
-  __device__ bool last_of_item() const { return tile + 1 == x.t1; }
-  __device__ void next(const KvAttnDev& A, int row_limit) {
-    if (--left <= 0) return;
-    if (++tile < x.t1) return;
-    if (++rt == RT) {
-      rt = 0;
-      if (++h == A.kv.H) {
-        h = 0;
-        do ++b;
-        while (b < A.kv.B && !takes(A, row_limit, b, s));
-        if (b >= A.kv.B) {  // cannot be: the run ends first
-          left = 0;
-          return;
-        }
-        RT = cdiv_i(s.n * A.G, kTM);
-      }
-    }
-    x = span_of(s, A.G, A.window, rt);
-    tile = x.t0;
-  }
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
@@ -184,11 +95,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, 1));
   return fmaxf(v, __shfl_xor_sync(FULL_MASK, v, 2));
@@ -207,68 +113,8 @@ __device__ __forceinline__ uint32_t place(int j, int c) {
   return j * D + ((c ^ ((j >> 1) & 3)) << 4);
 }
 
-// One row of an item again, key by key, over keys [ka, kb) with the row's own
-// final maximum m: o_d = sum over visible keys of exp2(s_j - m) v_jd.  dst16 (a
-// finished row, divided by the sum l) or dst32 (a partial).  One warp; rare.
 template <int DT, int FMT, int D>
-__device__ __noinline__ void redo_row(const KvAttnDev& A, int b, int h, const uint16_t* qrow, int p, int ka, int kb,
-                                      float m, float inv_l, uint16_t* dst16, float* dst32) {
-  constexpr int E = D / 32;  // values per lane
-  const int lane = threadIdx.x & 31;
-  const KvDev& P = A.kv;
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint32_t w = __ldg(qrow + lane * E + e);
-    float hi;
-    if (DT == SLORA_BF16) q[e] = __uint_as_float(w << 16);
-    else h2x2f(w, q[e], hi);
-    o[e] = 0.f;
-  }
-  if (A.window > 0) ka = max(ka, p - A.window + 1);
-  kb = min(kb, p + 1);
-  const unsigned char* base = reinterpret_cast<const unsigned char*>(P.pool);
-  for (int j = ka; j < kb; ++j) {
-    const uint32_t kr = kv_row(P, b, j, h);
-    if (kr == kNoRow) continue;
-    const uint32_t vr = kr + (uint32_t)(P.H * P.pt);
-    float kv[E], vv[E], dot = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (FMT == SLORA_KV_16) {
-        const uint32_t a = reinterpret_cast<const uint16_t*>(base)[(int64_t)kr * D + lane * E + e];
-        const uint32_t c = reinterpret_cast<const uint16_t*>(base)[(int64_t)vr * D + lane * E + e];
-        float hi;
-        if (DT == SLORA_BF16) {
-          kv[e] = __uint_as_float(a << 16);
-          vv[e] = __uint_as_float(c << 16);
-        } else {
-          h2x2f(a, kv[e], hi);
-          h2x2f(c, vv[e], hi);
-        }
-      } else {
-        const uint32_t a = e4m3x2_f16x2(base[(int64_t)kr * D + lane * E + e]);
-        const uint32_t c = e4m3x2_f16x2(base[(int64_t)vr * D + lane * E + e]);
-        kv[e] = __low2float(*reinterpret_cast<const __half2*>(&a)) * *kv_scale(P, kr);
-        vv[e] = __low2float(*reinterpret_cast<const __half2*>(&c)) * *kv_scale(P, vr);
-      }
-      dot += q[e] * kv[e];
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, d);
-    const float w = ex2(dot * A.c - m);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += w * vv[e];
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (dst16) dst16[lane * E + e] = (uint16_t)pack2<DT>(o[e] * inv_l, 0.f);
-    else dst32[lane * E + e] = o[e];
-  }
-}
-
-template <int DT, int FMT, int D>
-__global__ void __launch_bounds__(kNT, kCtasPerSm) k_kv_stream(const __grid_constant__ KvAttnDev A, int row_limit) {
+__global__ void __launch_bounds__(kNT, kCtasPerSm) k_kv_stream(const __grid_constant__ KvAttnDev A, RowClass cls) {
   using C = Cfg<FMT, D>;
   constexpr int MT = FMT == SLORA_KV_16 ? DT : SLORA_F16;  // operand type of the products
   constexpr int NB = D / 8;                                 // 8-column blocks of the output
@@ -289,52 +135,11 @@ __global__ void __launch_bounds__(kNT, kCtasPerSm) k_kv_stream(const __grid_cons
   if (blockIdx.x == 0) kv_record_bad(P, A.max_rows);
 
   // ---- this CTA's run of tiles
-  Cursor pc;
+  Cursor<kTM, kTK> pc;
   long long total, u1;
   int ctas;
-  {
-    long long* const sh = reinterpret_cast<long long*>(smem);
-    const long long mine0 = tid < P.B ? seq_tiles(A, row_limit, tid) : 0;
-    long long v = mine0;
-    for (int b = tid + kNT; b < P.B; b += kNT) v += seq_tiles(A, row_limit, b);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
-    if (lane == 0) sh[warp] = v;
-    __syncthreads();
-    total = sh[0] + sh[1] + sh[2] + sh[3];
-    __syncthreads();
-    ctas = (int)min((long long)gridDim.x, (total + kMinRun - 1) / kMinRun);
-    if ((int)blockIdx.x >= ctas) return;
-    const long long u0 = total * blockIdx.x / ctas;
-    u1 = total * (blockIdx.x + 1) / ctas;
-    long long base = 0;
-    for (int b0 = 0;; b0 += kNT) {  // the sequence that holds tile u0 (there is one: u0 < total)
-      const int b = b0 + tid;
-      const long long w = b0 == 0 ? mine0 : (b < P.B ? seq_tiles(A, row_limit, b) : 0);
-      long long inc = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(FULL_MASK, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) sh[warp] = inc;
-      __syncthreads();
-      long long before = base;
-      for (int i = 0; i < warp; ++i) before += sh[i];
-      base += sh[0] + sh[1] + sh[2] + sh[3];
-      if (w > 0 && before + inc - w <= u0 && u0 < before + inc) {
-        sh[4] = b;
-        sh[5] = u0 - (before + inc - w);
-      }
-      __syncthreads();
-      if (u0 < base) break;
-      __syncthreads();
-    }
-    pc.seek(A, row_limit, (int)sh[4], sh[5]);
-    pc.left = u1 - u0;
-    __syncthreads();
-  }
-  Cursor cc = pc;
+  if (!find_run<kTM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), pc, total, ctas, u1)) return;
+  Cursor<kTM, kTK> cc = pc;
   const int n_tiles = (int)pc.left;
 
   // ---- producer side: row numbers of tile i (ring), then its copies
@@ -357,7 +162,7 @@ __global__ void __launch_bounds__(kNT, kCtasPerSm) k_kv_stream(const __grid_cons
         const unsigned m = __ballot_sync(FULL_MASK, r != kNoRow);
         if (lane == 0) masks[(i % (S + 2)) * 2 + warp] = m;
       }
-      pc.next(A, row_limit);
+      pc.next(A, cls);
     }
   };
   auto copy = [&](int i) {
@@ -707,19 +512,12 @@ __global__ void __launch_bounds__(kNT, kCtasPerSm) k_kv_stream(const __grid_cons
       const bool complete = whole_end && seg_tile == cc.x.t0;
       const int slot = 2 * blockIdx.x + (segs > 0 ? 1 : 0);
       if (!whole_end && seg_tile == cc.x.t0 && tid == 0) {
-        // the partials of this item: this one, then one per run up to the run of its last tile
-        const long long end = u1 - cc.left + (cc.x.t1 - cc.tile);
-        const long long last = (end * ctas + total - 1) / total - 1;
-        split->b = cc.b;
-        split->h = cc.h;
-        split->rt = cc.rt;
-        split->slot = slot;
-        split->n = (int)(last - blockIdx.x) + 1;
+        note_split(split, cc.b, cc.h, cc.rt, slot, u1 - cc.left + (cc.x.t1 - cc.tile), total, ctas);
       }
       ++segs;
       if (kg == 0) {
-        float* const part = parts + (size_t)slot * slot_floats(D);
-        const float i0 = l0 > 0.f || l0 != l0 ? 1.f / l0 : 0.f, i1 = l1 > 0.f || l1 != l1 ? 1.f / l1 : 0.f;
+        float* const part = parts + (size_t)slot * slot_floats(kTM, D);
+        const float i0 = inverse(l0), i1 = inverse(l1);
         bool bad0 = false, bad1 = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -748,7 +546,7 @@ __global__ void __launch_bounds__(kNT, kCtasPerSm) k_kv_stream(const __grid_cons
                       make_uint2(pack2<DT>(o[nb][2 * rr] * inv, o[nb + 1][2 * rr] * inv),
                                  pack2<DT>(o[nb][2 * rr + 1] * inv, o[nb + 1][2 * rr + 1] * inv));
               }
-              if (A.lse && ql == 0) A.lse[tok * A.Hq + hq] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+              if (A.lse && ql == 0) A.lse[tok * A.Hq + hq] = lse_of(m, l);
             } else {
               if (FMT == SLORA_KV_16) {
 #pragma unroll
@@ -786,124 +584,44 @@ __global__ void __launch_bounds__(kNT, kCtasPerSm) k_kv_stream(const __grid_cons
         }
       }
     }
-    cc.next(A, row_limit);
+    cc.next(A, cls);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Joins the partials of the item that starts in run blockIdx.x and ends in a
-// later one: weights exp2(m_i - max m), in key order.  A warp per row.
-template <int DT, int D>
-__global__ void __launch_bounds__(kNT) k_kv_combine(KvAttnDev A) {
-  constexpr int E = D / 32;
-  griddep_wait();
-  const Split sp = reinterpret_cast<const Split*>(A.workspace)[blockIdx.x];
-  if (sp.n == 0) return;
-  const float* const parts = reinterpret_cast<const float*>(reinterpret_cast<const Split*>(A.workspace) + gridDim.x);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  KvSeq s;
-  kv_seq(A.kv, sp.b, A.max_rows, s);
-  const int r_item = sp.rt * kTM, R = min(s.n * A.G - r_item, kTM);
-  auto at = [&](int i) {
-    return parts + (size_t)(i == 0 ? sp.slot : 2 * ((int)blockIdx.x + i)) * slot_floats(D);
-  };
-  for (int r = blockIdx.y * 4 + warp; r < R; r += gridDim.y * 4) {
-    float top = -INFINITY;
-    for (int i = lane; i < sp.n; i += 32) top = fmaxf(top, at(i)[(size_t)kTM * D + r]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-    const float z = top == -INFINITY ? 0.f : top;
-    float l = 0.f, o[E] = {};
-    for (int i0 = 0; i0 < sp.n; i0 += 32) {
-      float w = 0.f, li = 0.f;
-      if (i0 + lane < sp.n) {
-        w = ex2(at(i0 + lane)[(size_t)kTM * D + r] - z);
-        li = w * at(i0 + lane)[(size_t)kTM * (D + 1) + r];
-      }
-      const int n = min(32, sp.n - i0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(FULL_MASK, w, i);
-        l += __shfl_sync(FULL_MASK, li, i);
-        const float* p = at(i0 + i) + (size_t)r * D + lane * E;
-        if (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(p);
-          o[0] += wi * v.x;
-          o[1] += wi * v.y;
-          o[E - 2] += wi * v.z;
-          o[E - 1] += wi * v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(p);
-          o[0] += wi * v.x;
-          o[1] += wi * v.y;
-        }
-      }
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int t = (r_item + r) / A.G, hq = sp.h * A.G + (r_item + r) - t * A.G;
-    const int64_t tok = s.row0 + t;
-    uint16_t* const orow = A.out + tok * A.ldo + (int64_t)hq * D + lane * E;
-    if (E == 4)
-      *reinterpret_cast<uint2*>(orow) = make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[E - 2] * inv, o[E - 1] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(orow) = pack2<DT>(o[0] * inv, o[1] * inv);
-    if (A.lse && lane == 0) A.lse[tok * A.Hq + hq] = l == 0.f ? -INFINITY : (top + __log2f(l)) * kLn2;
-  }
-}
-
 template <int DT, int FMT, int D>
-cudaError_t run_stream(const KvAttnDev& A, int sm_count, int row_limit, cudaStream_t st) {
+cudaError_t run_stream(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream_t st) {
   using C = Cfg<FMT, D>;
   const int grid = sm_count * kCtasPerSm;
-  auto kern = k_kv_stream<DT, FMT, D>;
   static std::atomic<bool> sized[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_stream<DT, FMT, D>), C::kSmem, sized);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!sized[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    sized[dev] = true;
-  }
-  kern<<<grid, kNT, C::kSmem, st>>>(A, row_limit);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 4);
-  cfg.blockDim = dim3(kNT);
-  cfg.stream = st;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv_combine<DT, D>, A);
+  k_kv_stream<DT, FMT, D><<<grid, kNT, C::kSmem, st>>>(A, cls);
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 != cudaSuccess ? e2 : launch_combine<DT, D, kTM>(A, grid, st);
 }
 
 }  // namespace
 
-size_t kv_attention_workspace(int D, int G, int max_rows, int sm_count) {
-  (void)G;
-  (void)max_rows;
+size_t kv_stream_workspace(int D, int sm_count) {
   const size_t ctas = (size_t)sm_count * kCtasPerSm;
-  return ctas * sizeof(Split) + 2 * ctas * slot_floats(D) * 4;
+  return ctas * sizeof(Split) + 2 * ctas * slot_floats(kTM, D) * 4;
 }
 
-cudaError_t launch_kv_attention(const KvAttnDev& A, int dtype, int fmt, int D, int sm_count, cudaStream_t s) {
-  const int lim = INT32_MAX;
+cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s) {
+  const RowClass cls = {0, row_limit};
   if (D == 128) {
     if (dtype == SLORA_F16)
-      return fmt == SLORA_KV_16 ? run_stream<SLORA_F16, SLORA_KV_16, 128>(A, sm_count, lim, s)
-                                : run_stream<SLORA_F16, SLORA_KV_E4M3, 128>(A, sm_count, lim, s);
-    return fmt == SLORA_KV_16 ? run_stream<SLORA_BF16, SLORA_KV_16, 128>(A, sm_count, lim, s)
-                              : run_stream<SLORA_BF16, SLORA_KV_E4M3, 128>(A, sm_count, lim, s);
+      return fmt == SLORA_KV_16 ? run_stream<SLORA_F16, SLORA_KV_16, 128>(A, sm_count, cls, s)
+                                : run_stream<SLORA_F16, SLORA_KV_E4M3, 128>(A, sm_count, cls, s);
+    return fmt == SLORA_KV_16 ? run_stream<SLORA_BF16, SLORA_KV_16, 128>(A, sm_count, cls, s)
+                              : run_stream<SLORA_BF16, SLORA_KV_E4M3, 128>(A, sm_count, cls, s);
   }
   if (dtype == SLORA_F16)
-    return fmt == SLORA_KV_16 ? run_stream<SLORA_F16, SLORA_KV_16, 64>(A, sm_count, lim, s)
-                              : run_stream<SLORA_F16, SLORA_KV_E4M3, 64>(A, sm_count, lim, s);
-  return fmt == SLORA_KV_16 ? run_stream<SLORA_BF16, SLORA_KV_16, 64>(A, sm_count, lim, s)
-                            : run_stream<SLORA_BF16, SLORA_KV_E4M3, 64>(A, sm_count, lim, s);
+    return fmt == SLORA_KV_16 ? run_stream<SLORA_F16, SLORA_KV_16, 64>(A, sm_count, cls, s)
+                              : run_stream<SLORA_F16, SLORA_KV_E4M3, 64>(A, sm_count, cls, s);
+  return fmt == SLORA_KV_16 ? run_stream<SLORA_BF16, SLORA_KV_16, 64>(A, sm_count, cls, s)
+                            : run_stream<SLORA_BF16, SLORA_KV_E4M3, 64>(A, sm_count, cls, s);
 }
 
 }  // namespace slora

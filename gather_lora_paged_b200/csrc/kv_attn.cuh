@@ -1,0 +1,346 @@
+// kv_attn.cuh -- what the attention kernels share (kv_attention.cu,
+// kv_chunk.cu): the line of key tiles that is cut into one run per CTA, the
+// join of the partials, the row that is summed again.
+//
+// The rows of a kv head are the n * G pairs (token, head of the group), in row
+// tiles of TM.  A work item is (sequence, kv head, row tile); its keys come in
+// tiles of TK, and the tiles of all items, laid out in one line, are cut into
+// equal runs, one per CTA, so that ragged lengths and a single long sequence
+// keep every SM equally busy.  An item inside one run is finished there; one that
+// crosses runs leaves (max, sum, unnormalised row) partials, at most two per
+// CTA, and k_kv_combine joins them in key order.
+#pragma once
+
+#include <atomic>
+
+#include "kv_common.cuh"
+
+namespace slora {
+namespace {
+
+// Lets a kernel have its dynamic shared memory, once per device.
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load()) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[dev].store(true);
+  return e;
+}
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+// The sequences a kernel takes: those with row_lo < rows per kv head <= row_hi.
+struct RowClass {
+  int lo, hi;
+};
+
+// A split item, written by the CTA whose run holds its first tile.
+struct Split {
+  int b, h, rt, slot;  // the first partial; the others are the even slots of the next CTAs
+  int n;               // partials (0: none)
+  int pad[3];
+};
+
+__host__ __device__ inline size_t slot_floats(int TM, int D) { return (size_t)TM * (D + 2); }
+
+struct Span {
+  int lo, hi;       // keys some row of the tile sees
+  int t0, t1;       // key tiles (at least one)
+};
+
+// Keys of rows [rt * TM, ...) of a sequence.
+template <int TM, int TK>
+__device__ __forceinline__ Span span_of(const KvSeq& s, int G, int window, int rt) {
+  const int R = s.n * G, r0 = rt * TM, r1 = min(R, r0 + TM) - 1;
+  const int first = s.len - s.n;
+  Span x;
+  x.hi = max(0, first + r1 / G + 1);
+  x.lo = window > 0 ? max(0, first + r0 / G - window + 1) : 0;
+  x.t0 = x.lo / TK;
+  x.t1 = max(x.t0 + 1, (x.hi + TK - 1) / TK);
+  return x;
+}
+__device__ __forceinline__ bool takes(const KvAttnDev& A, RowClass cls, int b, KvSeq& s) {
+  if (!kv_seq(A.kv, b, A.max_rows, s)) return false;
+  const int64_t R = (int64_t)s.n * A.G;
+  return R > cls.lo && R <= cls.hi;
+}
+// Tiles of all items of sequence b.
+template <int TM, int TK>
+__device__ __forceinline__ long long seq_tiles(const KvAttnDev& A, RowClass cls, int b) {
+  KvSeq s;
+  if (!takes(A, cls, b, s)) return 0;
+  const int RT = cdiv_i(s.n * A.G, TM);
+  long long u = 0;
+  for (int rt = 0; rt < RT; ++rt) {
+    const Span x = span_of<TM, TK>(s, A.G, A.window, rt);
+    u += x.t1 - x.t0;
+  }
+  return u * A.kv.H;
+}
+
+// A place in the line of tiles.
+template <int TM, int TK>
+struct Cursor {
+  KvSeq s;
+  Span x;
+  int b, h, rt, RT, tile;
+  long long left;  // tiles of this CTA from here on
+
+  __device__ void seek(const KvAttnDev& A, RowClass cls, int b_, long long off) {
+    b = b_;
+    takes(A, cls, b, s);
+    RT = cdiv_i(s.n * A.G, TM);
+    long long per = 0;
+    for (rt = 0; rt < RT; ++rt) {
+      x = span_of<TM, TK>(s, A.G, A.window, rt);
+      per += x.t1 - x.t0;
+    }
+    h = (int)(off / per);
+    off -= h * per;
+    for (rt = 0;; ++rt) {
+      x = span_of<TM, TK>(s, A.G, A.window, rt);
+      if (off < x.t1 - x.t0) break;
+      off -= x.t1 - x.t0;
+    }
+    tile = x.t0 + (int)off;
+  }
+  __device__ bool last_of_item() const { return tile + 1 == x.t1; }
+  __device__ bool next(const KvAttnDev& A, RowClass cls) {  // false: the run is over
+    if (--left <= 0) return false;
+    if (++tile < x.t1) return true;
+    if (++rt == RT) {
+      rt = 0;
+      if (++h == A.kv.H) {
+        h = 0;
+        do ++b;
+        while (b < A.kv.B && !takes(A, cls, b, s));
+        if (b >= A.kv.B) {  // cannot be: the run ends first
+          left = 0;
+          return false;
+        }
+        RT = cdiv_i(s.n * A.G, TM);
+      }
+    }
+    x = span_of<TM, TK>(s, A.G, A.window, rt);
+    tile = x.t0;
+    return true;
+  }
+};
+
+// This CTA's run of the line (all NT threads; sh: NT / 32 + 2 words of shared
+// memory, free again afterwards).  Runs are at least min_run tiles on average.
+// False: this CTA has none.  total, ctas, u1: tiles in the line, runs, this run's end.
+template <int TM, int TK, int NT>
+__device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_run, long long* sh,
+                                         Cursor<TM, TK>& c, long long& total, int& ctas, long long& u1) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = A.kv.B;
+  const long long mine0 = tid < B ? seq_tiles<TM, TK>(A, cls, tid) : 0;
+  long long v = mine0;
+  for (int b = tid + NT; b < B; b += NT) v += seq_tiles<TM, TK>(A, cls, b);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+  if (lane == 0) sh[warp] = v;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) total += sh[i];
+  __syncthreads();
+  ctas = (int)min((long long)gridDim.x, (total + min_run - 1) / min_run);
+  if ((int)blockIdx.x >= ctas) return false;
+  const long long u0 = total * blockIdx.x / ctas;
+  u1 = total * (blockIdx.x + 1) / ctas;
+  long long base = 0;
+  for (int b0 = 0;; b0 += NT) {  // the sequence that holds tile u0 (there is one: u0 < total)
+    const int b = b0 + tid;
+    const long long w = b0 == 0 ? mine0 : (b < B ? seq_tiles<TM, TK>(A, cls, b) : 0);
+    long long inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(FULL_MASK, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) sh[warp] = inc;
+    __syncthreads();
+    long long before = base;
+    for (int i = 0; i < warp; ++i) before += sh[i];
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) base += sh[i];
+    if (w > 0 && before + inc - w <= u0 && u0 < before + inc) {
+      sh[NT / 32] = b;
+      sh[NT / 32 + 1] = u0 - (before + inc - w);
+    }
+    __syncthreads();
+    if (u0 < base) break;
+  }
+  c.seek(A, cls, (int)sh[NT / 32], sh[NT / 32 + 1]);
+  c.left = u1 - u0;
+  __syncthreads();
+  return true;
+}
+
+// Partials of an item whose first tile is in this run (slot: this CTA's) and
+// whose last tile is number end - 1 of the line.
+__device__ __forceinline__ void note_split(Split* sp, int b, int h, int rt, int slot, long long end, long long total,
+                                           int ctas) {
+  const long long last = (end * ctas + total - 1) / total - 1;  // the run of tile end - 1
+  sp->b = b;
+  sp->h = h;
+  sp->rt = rt;
+  sp->slot = slot;
+  sp->n = (int)(last - blockIdx.x) + 1;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
+// 1 / sum, 0 for a row without keys (a NaN sum stays NaN).
+__device__ __forceinline__ float inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
+
+// One row of an item again, key by key, over keys [ka, kb) with the row's own
+// final maximum m: o_d = sum over visible keys of exp2(s_j - m) v_jd.  dst16 (a
+// finished row, divided by the sum l) or dst32 (a partial).  One warp; rare.
+template <int DT, int FMT, int D>
+__device__ __noinline__ void redo_row(const KvAttnDev& A, int b, int h, const uint16_t* qrow, int p, int ka, int kb,
+                                      float m, float inv_l, uint16_t* dst16, float* dst32) {
+  constexpr int E = D / 32;  // values per lane
+  const int lane = threadIdx.x & 31;
+  const KvDev& P = A.kv;
+  float q[E], o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint32_t w = __ldg(qrow + lane * E + e);
+    float hi;
+    if (DT == SLORA_BF16) q[e] = __uint_as_float(w << 16);
+    else h2x2f(w, q[e], hi);
+    o[e] = 0.f;
+  }
+  if (A.window > 0) ka = max(ka, p - A.window + 1);
+  kb = min(kb, p + 1);
+  const unsigned char* base = reinterpret_cast<const unsigned char*>(P.pool);
+  for (int j = ka; j < kb; ++j) {
+    const uint32_t kr = kv_row(P, b, j, h);
+    if (kr == kNoRow) continue;
+    const uint32_t vr = kr + (uint32_t)(P.H * P.pt);
+    float kv[E], vv[E], dot = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (FMT == SLORA_KV_16) {
+        const uint32_t a = reinterpret_cast<const uint16_t*>(base)[(int64_t)kr * D + lane * E + e];
+        const uint32_t c = reinterpret_cast<const uint16_t*>(base)[(int64_t)vr * D + lane * E + e];
+        float hi;
+        if (DT == SLORA_BF16) {
+          kv[e] = __uint_as_float(a << 16);
+          vv[e] = __uint_as_float(c << 16);
+        } else {
+          h2x2f(a, kv[e], hi);
+          h2x2f(c, vv[e], hi);
+        }
+      } else {
+        const uint32_t a = e4m3x2_f16x2(base[(int64_t)kr * D + lane * E + e]);
+        const uint32_t c = e4m3x2_f16x2(base[(int64_t)vr * D + lane * E + e]);
+        kv[e] = __low2float(*reinterpret_cast<const __half2*>(&a)) * *kv_scale(P, kr);
+        vv[e] = __low2float(*reinterpret_cast<const __half2*>(&c)) * *kv_scale(P, vr);
+      }
+      dot += q[e] * kv[e];
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, d);
+    const float w = ex2(dot * A.c - m);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += w * vv[e];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (dst16) dst16[lane * E + e] = (uint16_t)pack2<DT>(o[e] * inv_l, 0.f);
+    else dst32[lane * E + e] = o[e];
+  }
+}
+
+// Joins the partials of the item that starts in run blockIdx.x and ends in a
+// later one: weights exp2(m_i - max m), in key order.  A warp per row.
+constexpr int kCombineThreads = 128;
+template <int DT, int D, int TM>
+__global__ void __launch_bounds__(kCombineThreads) k_kv_combine(KvAttnDev A) {
+  constexpr int E = D / 32;
+  griddep_wait();
+  const Split sp = reinterpret_cast<const Split*>(A.workspace)[blockIdx.x];
+  if (sp.n == 0) return;
+  const float* const parts = reinterpret_cast<const float*>(reinterpret_cast<const Split*>(A.workspace) + gridDim.x);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  KvSeq s;
+  kv_seq(A.kv, sp.b, A.max_rows, s);
+  const int r_item = sp.rt * TM, R = min(s.n * A.G - r_item, TM);
+  auto at = [&](int i) {
+    return parts + (size_t)(i == 0 ? sp.slot : 2 * ((int)blockIdx.x + i)) * slot_floats(TM, D);
+  };
+  for (int r = blockIdx.y * 4 + warp; r < R; r += gridDim.y * 4) {
+    float top = -INFINITY;
+    for (int i = lane; i < sp.n; i += 32) top = fmaxf(top, at(i)[(size_t)TM * D + r]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+    const float z = top == -INFINITY ? 0.f : top;
+    float l = 0.f, o[E] = {};
+    for (int i0 = 0; i0 < sp.n; i0 += 32) {
+      float w = 0.f, li = 0.f;
+      if (i0 + lane < sp.n) {
+        w = ex2(at(i0 + lane)[(size_t)TM * D + r] - z);
+        li = w * at(i0 + lane)[(size_t)TM * (D + 1) + r];
+      }
+      const int n = min(32, sp.n - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(FULL_MASK, w, i);
+        l += __shfl_sync(FULL_MASK, li, i);
+        const float* p = at(i0 + i) + (size_t)r * D + lane * E;
+        if (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(p);
+          o[0] += wi * v.x;
+          o[1] += wi * v.y;
+          o[E - 2] += wi * v.z;
+          o[E - 1] += wi * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(p);
+          o[0] += wi * v.x;
+          o[1] += wi * v.y;
+        }
+      }
+    }
+    const float inv = inverse(l);
+    const int t = (r_item + r) / A.G, hq = sp.h * A.G + (r_item + r) - t * A.G;
+    const int64_t tok = s.row0 + t;
+    uint16_t* const orow = A.out + tok * A.ldo + (int64_t)hq * D + lane * E;
+    if (E == 4)
+      *reinterpret_cast<uint2*>(orow) = make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[E - 2] * inv, o[E - 1] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(orow) = pack2<DT>(o[0] * inv, o[1] * inv);
+    if (A.lse && lane == 0) A.lse[tok * A.Hq + hq] = lse_of(top, l);
+  }
+}
+
+
+// Launches the join behind the kernel that writes the partials (a programmatic
+// dependent launch: its CTAs are in place when that kernel ends).
+template <int DT, int D, int TM>
+cudaError_t launch_combine(const KvAttnDev& A, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, TM / 16);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_kv_combine<DT, D, TM>, A);
+}
+
+}  // namespace
+}  // namespace slora

@@ -1265,11 +1265,18 @@ slora_status_t slora_kv_read(slora_pool* P, const slora_kv_layout_t* layout, voi
   return SLORA_OK;
 }
 
+// Whether a sequence of the call may have more rows per kv head than the stream
+// kernel takes.
+static bool kv_has_chunks(int G, int max_rows) { return (int64_t)G * max_rows > kKvStreamRows; }
+
 size_t slora_kv_attention_workspace_bytes(const slora_pool* P, const slora_kv_layout_t* layout, int32_t n_q_heads,
                                           int32_t B, int32_t T, int32_t max_rows) {
   if (!P || !kv_layout_ok(layout) || n_q_heads < 1 || n_q_heads % layout->n_kv_heads || B < 1 || T < 1 || max_rows < 1)
     return 0;
-  return kv_attention_workspace(layout->head_dim, n_q_heads / layout->n_kv_heads, std::min(max_rows, T), P->sm_count);
+  const size_t stream = kv_stream_workspace(layout->head_dim, P->sm_count);
+  return kv_has_chunks(n_q_heads / layout->n_kv_heads, std::min(max_rows, T))
+             ? std::max(stream, kv_chunk_workspace(layout->head_dim, P->sm_count))
+             : stream;
 }
 
 slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout, int32_t n_q_heads, const void* q,
@@ -1309,7 +1316,9 @@ slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout
   A.workspace = workspace;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   phase(P, 0, 1, st);
-  CUDA_TRY(P, launch_kv_attention(A, P->d.dtype, layout->format, layout->head_dim, P->sm_count, st));
+  CUDA_TRY(P, launch_kv_stream(A, P->d.dtype, layout->format, layout->head_dim, kKvStreamRows, P->sm_count, st));
+  if (kv_has_chunks(A.G, A.max_rows))
+    CUDA_TRY(P, launch_kv_chunk(A, P->d.dtype, layout->format, layout->head_dim, kKvStreamRows, P->sm_count, st));
   phase(P, 1, 1, st);
   return SLORA_OK;
 }

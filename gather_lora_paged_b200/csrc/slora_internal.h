@@ -190,7 +190,11 @@ cudaError_t launch_kv_write(const KvDev& P, int dtype, int fmt, int D, const voi
                             int64_t ldv, int sm_count, cudaStream_t s);
 cudaError_t launch_kv_read(const KvDev& P, int dtype, int fmt, int D, void* k, int64_t ldk, void* v, int64_t ldv,
                            int sm_count, cudaStream_t s);
-cudaError_t launch_kv_attention(const KvAttnDev& A, int dtype, int fmt, int D, int sm_count, cudaStream_t s);
-size_t kv_attention_workspace(int D, int G, int max_rows, int sm_count);
+// Sequences of at most row_limit rows per kv head (kv_attention.cu), and of more (kv_chunk.cu).
+constexpr int kKvStreamRows = 64;
+cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s);
+size_t kv_stream_workspace(int D, int sm_count);
+cudaError_t launch_kv_chunk(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s);
+size_t kv_chunk_workspace(int D, int sm_count);
 
 }  // namespace slora
