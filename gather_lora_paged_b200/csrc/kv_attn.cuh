@@ -1,4 +1,4 @@
-// kv_attn.cuh -- what the attention kernels share (kv_attention.cu,
+// kv_attn.cuh -- what the attention kernels share (kv_decode.cu,
 // kv_chunk.cu): the line of key tiles that is cut into one run per CTA, the
 // join of the partials, the row that is summed again.
 //
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_kv_combine(KvAttnDev A) {
 template <int DT, int D, int TM>
 cudaError_t launch_combine(const KvAttnDev& A, int grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, TM / 16);
+  cfg.gridDim = dim3(grid, TM >= 16 ? TM / 16 : 1);
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = st;
   cudaLaunchAttribute at = {};

@@ -1,6 +1,6 @@
 // kv_chunk.cu -- attention of prompt chunks (more than 64 rows per kv head) over
 // the KV pages on the 5th-generation tensor cores.  Definition and row order as
-// in kv_attention.cu; runs, partials and their join as in kv_attn.cuh.
+// in kv_decode.cu; runs, partials and their join as in kv_attn.cuh.
 //
 // One CTA per SM, 12 warps; an item is 256 rows (token, head of the group) of
 // one kv head as two M = 128 tiles, its keys come 128 at a time:
@@ -20,7 +20,7 @@
 // fp16's range, and the accumulator in TMEM is read and scaled on few tiles.
 // Sums and statistics are fp32 and of the unrounded weights; the weights are
 // rounded once to the operand type, which puts an error of the size of the output's own
-// rounding on it (the two halves of kv_attention.cu would double the P.V
+// rounding on it (the two halves of kv_decode.cu would double the P.V
 // product, which is half the work here).
 // e4m3: K's scale multiplies the score, V's the weight, relative to a V scale
 // that is raised when a tile's largest is 8 times it.
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int x = lw + kLoadWarps * (lane + 32 * q), j = tile * kTK + x;
-          pg[q] = x < kTK && j >= c.x.lo && j < c.x.hi ? __ldg(P.blocks + (int64_t)c.b * P.ldb + j / P.pt) : 0;
+          pg[q] = x < kTK && j >= c.x.lo && j < c.x.hi ? __ldg(P.blocks + (int64_t)c.b * P.ldb + kv_block(P, j)) : 0;
         }
       };
       auto resolve = [&](int tile, uint32_t t) {  // the tile's rows from pg; t: its number
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           const int x = lw + kLoadWarps * (lane + 32 * q), j = tile * kTK + x;
           uint32_t r = kNoRow;
           if (x < kTK && j >= c.x.lo && j < c.x.hi) {
-            if (pg[q] >= 0 && pg[q] < P.n_pages) r = ((uint32_t)pg[q] << P.row_shift) + (uint32_t)(c.h * P.pt + j % P.pt);
+            if (pg[q] >= 0 && pg[q] < P.n_pages) r = ((uint32_t)pg[q] << P.row_shift) + (uint32_t)(c.h * P.pt + j - kv_block(P, j) * P.pt);
             else bad |= 1u << q;
           }
           rows_of[lane + 32 * q] = r;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           if (FMT == SLORA_KV_16 || DT == SLORA_F16) {
             cp16(dst, src, real);
             if (FMT == SLORA_KV_E4M3 && ch == 0) qscale[(qi & 1) * kTM + r] = A.c;
-          } else {  // a bf16 row as fp16 times a power of two (see kv_attention.cu)
+          } else {  // a bf16 row as fp16 times a power of two (see kv_decode.cu)
             const uint4 v = real ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t top = 0;

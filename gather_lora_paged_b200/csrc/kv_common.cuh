@@ -1,5 +1,5 @@
 // kv_common.cuh -- what the KV-cache kernels share (kv_cache.cu,
-// kv_attention.cu, kv_chunk.cu): their parameter blocks, the layout of a KV page, the
+// kv_decode.cu, kv_chunk.cu): their parameter blocks, the layout of a KV page, the
 // checks of a batch's sequences, e4m3 conversions.
 //
 // A page of one layer holds page_tokens tokens of H kv heads, as rows of D
@@ -51,10 +51,15 @@ __device__ __forceinline__ void kv_record_bad(const KvDev& P, int max_rows) {
   }
 }
 
+// Page of a sequence that holds a position.
+__device__ __forceinline__ int kv_block(const KvDev& P, int pos) {
+  return (int)(((uint64_t)(uint32_t)pos * P.pt_mul) >> P.pt_shift);
+}
+
 // Row of (sequence b, position pos, K part, head h) in the pool; kNoRow (and a
 // recorded error) if its page id is outside the pool.  The V row is H * pt on.
 __device__ __forceinline__ uint32_t kv_row(const KvDev& P, int b, int pos, int h) {
-  const int blk = pos / P.pt;
+  const int blk = kv_block(P, pos);
   const int pg = __ldg(P.blocks + (int64_t)b * P.ldb + blk);
   if (pg < 0 || pg >= P.n_pages) {
     record_error(P.err, kErrKvPage, b);

@@ -1,0 +1,896 @@
+// kv_decode.cu -- attention of each sequence's newest tokens over its KV pages,
+// for few rows per kv head (decode, drafted tokens): a stream of the cache
+// through the 5th-generation tensor cores, scores and output transposed.
+//
+// For query row i of a sequence (position p_i = kv_len - n + i) and query head
+// hq reading kv head h = hq / G:
+//     o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale * q_i . k_j),
+//     j <= p_i and, with a window, j > p_i - window;
+//     lse_i = log sum_j w_ij;  a row that sees no key gets 0 and -inf.
+//
+// HBM bounds this: each cached row is read once per row tile and met by few rows, so
+// that instructions spent per cached byte decide.  With the keys on the MMA's M side,
+//     S^T [128 keys x rows] = K . Q^T,   O^T [D x rows] += V^T . W^T,
+// a tile of 128 keys goes from the pages to shared memory (16-byte cp.async, a page may hold
+// one token, so rows are gathered) and from there straight to the tensor cores:
+// no thread touches a cached element, and the rows only fill N, a multiple of 16.
+// Items, runs, partials and their join: kv_attn.cuh.
+//
+// One CTA per SM, 16 warps:
+//   warps 4..7  copy K and V rows into a ring of slots (K or V of a tile), 32 keys
+//               each; the copies signal the slot's barrier when they land;
+//   warp 9      the run's items, for all others;
+//   warp 10     q of the items ahead, as the N side of S^T, and the rows' positions;
+//   warp 8      issues S^T of tile i + 1, then O^T of tile i;
+//   warps 0..3  the softmax: a thread owns a key, reads its scores from TMEM and
+//               writes its weights to shared memory as the N side of O^T;
+//   warps 12..15  an item's end: O^T from TMEM to the output, beside the next item.
+//
+// Weights are exp(s - m) with m a former maximum of the row: it moves (and O^T is
+// scaled) only when a score exceeds it by 2^3, which one vote per tile finds out.
+//
+// What the tensor cores take is split so that nothing is lost that an output could show:
+// 16-bit: weights as hi + lo, two 16-bit columns of N.
+// e4m3:   the codes are operands as they are (kind::f8f6f4), and q and the weights
+//         are sums of three e4m3 values, each 2^-4 of the one before and a
+//         column of its own: 12 bits, so an fp16 q is exact.  The largest of a q row lies in
+//         [2^7, 2^8) after a power of two, what is lost of any element is under 2^-26 of it;
+//         the weights reach 2^5 at m and 2^8 at most, what is lost is under 2^-23 of the
+//         row's largest.  K's row scale multiplies the score, V's the weight, relative to
+//         twice the largest V scale met so far.
+//
+// A key that a row does not see has weight 0, but 0 * inf is NaN: where a
+// masked V row holds an infinity or a NaN, the rows that it spoiled are seen to be not
+// finite at the end and are summed again key by key, without the masked keys.
+#include <math.h>
+
+#include "kv_attn.cuh"
+#include "kv_tc.cuh"
+
+namespace slora {
+namespace {
+
+constexpr int kNT = 512;       // threads
+constexpr int kTK = 128;       // keys per tile
+constexpr int kMinRun = 1;     // tiles that are worth a CTA of their own
+constexpr int kMeta = 8;       // tiles whose scales and masks are kept: what the ring holds, at least
+constexpr int kItems = 16;     // items that are known ahead
+constexpr float kSlack = 3.f;  // log2 by which scores may exceed the row's reference
+constexpr float kLift = 32.f;  // weight at the reference
+
+// TM: rows per item.  N is a multiple of 16 rows (e4m3: three columns a row).
+template <int FMT, int D, int TM>
+struct Cfg {
+  static constexpr bool kF8 = FMT == SLORA_KV_E4M3;
+  static constexpr int kRow = KvRow<FMT, D>::kBytes;                    // a cached row
+  static constexpr int kWidth = kRow >= 128 ? 128 : kRow;               // bytes of a row in a panel
+  static constexpr int kPanel = kTK * kWidth;
+  static constexpr int kSlot = kTK * kRow;                              // K or V of a tile
+  static constexpr int kRows16 = (TM + 15) / 16 * 16;
+  static constexpr int kQRows = kF8 ? 3 * kRows16 : kRows16;            // columns of S^T
+  static constexpr int kPCols = kF8 ? 3 * kRows16 : 2 * TM;             // columns of O^T
+  static constexpr int kQ = kQRows * kRow;                              // one of two buffers
+  static constexpr int kP = kPCols * (kF8 ? 1 : 2) * kTK;               // one of two buffers
+  static constexpr int kSlots = kF8 ? (D == 64 ? 16 : (TM <= 16 ? 10 : 8)) : (D == 64 ? 10 : (TM <= 16 ? 6 : 5));
+  static constexpr int kOffP = kSlots * kSlot;
+  static constexpr int kOffQ = kOffP + 2 * kP;
+  static constexpr int kOffScale = kOffQ + 2 * kQ;
+  static constexpr int kScale = kF8 ? kMeta * 2 * kTK * 4 : 0;
+  static constexpr int kOffCtl = kOffScale + kScale;
+  static constexpr int kSCols = kQRows;                                 // TMEM: S0, S1, O's
+  static constexpr int kOBufs = 2 * (kSCols + kPCols) <= 512 ? 2 : 1;   // items' O^T side by side
+  static constexpr int kTmemCols = 2 * kSCols + kOBufs * kPCols;
+  static constexpr int kTmem = kTmemCols <= 64 ? 64 : kTmemCols <= 128 ? 128 : kTmemCols <= 256 ? 256 : 512;
+  static_assert(kSlots <= 2 * kMeta, "an entry is written again once V's slot of that tile is free");
+  static_assert(kTmemCols <= 512, "TMEM");
+};
+
+// What a run has to do, one entry per item, written by one warp for the others.
+struct Item {
+  int b, h, rt, R;        // sequence, kv head, row tile, rows
+  int row0, first;        // the sequence's first row and that row's position
+  int lo, hi;             // keys some row sees
+  int tile, n_tiles;      // this run's tiles of the item
+  int flags;              // 1: it starts here, 2: it ends here, 4: the run's last
+  int pad;
+};
+
+template <int TM, int S>
+struct Ctl {
+  uint64_t kv_full[S], kv_empty[S], q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], rows_full[kItems];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], sum_full[2], fin;
+  Item item[kItems];
+  uint32_t tmem;
+  int dead;                                   // a wait gave up: nobody waits any more
+  uint32_t mask[kMeta][4];                    // keys of a tile that are there
+  float qmul[kItems][(TM + 15) / 16 * 16];    // score multipliers of an item's rows
+  int pos[kItems][(TM + 15) / 16 * 16];       // their positions (-1: no such row)
+  float red[4][TM + 4];                       // warps' maxima
+  float ref[TM];                              // the rows' references
+  float fac[TM];                              // what a move of them scales sums by
+  // an item's end, for the epilogue: warps' sums, references, the weights' unit, and its own notes
+  float sum[2][4][TM], end_ref[2][TM], unit[2], out_fac[TM];
+  uint32_t bad[4][2];                         // warps' rows that are not finite
+};
+
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t dst, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(a) : "memory");
+}
+__device__ __forceinline__ void ld8(uint32_t taddr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void st8(uint32_t taddr, const float* v) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(u[0]),
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+// tcgen05.wait::ld, tied to the registers that the load fills
+__device__ __forceinline__ void wait_ld8(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The softmax warps' and the epilogue warps' barriers, and votes over them.
+template <int ID>
+__device__ __forceinline__ void sync_four() { asm volatile("barrier.sync %0, 128;" ::"n"(ID) : "memory"); }
+template <int ID>
+__device__ __forceinline__ bool any_of_four(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.red.or.pred b, %2, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r) : "r"((uint32_t)p), "n"(ID) : "memory");
+  return r;
+}
+__device__ __forceinline__ void softmax_sync() { sync_four<1>(); }
+__device__ __forceinline__ bool softmax_any(bool p) { return any_of_four<2>(p); }
+__device__ __forceinline__ void epilogue_sync() { sync_four<3>(); }
+__device__ __forceinline__ bool epilogue_any(bool p) { return any_of_four<4>(p); }
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Two values as three e4m3 codes each, every one 2^-4 of the one before.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  float x, y;
+  p0 = e4m3x2(a, b);
+  h2x2f(e4m3x2_f16x2(p0), x, y);
+  a = (a - x) * 16.f;
+  b = (b - y) * 16.f;
+  p1 = e4m3x2(a, b);
+  h2x2f(e4m3x2_f16x2(p1), x, y);
+  p2 = e4m3x2((a - x) * 16.f, (b - y) * 16.f);
+}
+
+// Byte offset of 16-byte chunk c of row j, in panels of `rows` rows of W bytes.
+template <int W>
+__device__ __forceinline__ uint32_t place(int rows, int j, int c) {
+  if (W == 128) return (uint32_t)((c >> 3) * rows * 128 + j * 128 + (((c & 7) ^ (j & 7)) << 4));
+  return (uint32_t)(j * 64 + ((c ^ ((j >> 1) & 3)) << 4));
+}
+
+template <int DT, int FMT, int D, int TM>
+__global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ KvAttnDev A, RowClass cls) {
+  using C = Cfg<FMT, D, TM>;
+  constexpr int S = C::kSlots, W = C::kWidth;
+  constexpr bool F8 = C::kF8;
+  using Control = Ctl<TM, S>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* const smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = su32(smem);
+  Control* const ctl = reinterpret_cast<Control*>(smem + C::kOffCtl);
+  const KvDev& P = A.kv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Split* const split = reinterpret_cast<Split*>(A.workspace) + blockIdx.x;
+  float* const parts = reinterpret_cast<float*>(reinterpret_cast<Split*>(A.workspace) + gridDim.x);
+
+  griddep_launch();  // the join's CTAs may take their places (they wait for this grid's end)
+  if (tid == 0) split->n = 0;
+  if (blockIdx.x == 0) kv_record_bad(P, A.max_rows);
+  Cursor<TM, kTK> c;
+  long long total, u1;
+  int ctas;
+  if (!find_run<TM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) return;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      for (int i = 0; i < S; ++i) {
+        bar_init(&ctl->kv_full[i], 128 + 4);
+        bar_init(&ctl->kv_empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        bar_init(&ctl->q_full[i], 64);
+        bar_init(&ctl->q_empty[i], 1);
+        bar_init(&ctl->s_full[i], 1);
+        bar_init(&ctl->p_full[i], 128);
+        bar_init(&ctl->pv_done[i], 1);
+        bar_init(&ctl->o_full[i], 1);
+        bar_init(&ctl->o_empty[i], 128);
+        bar_init(&ctl->sum_full[i], 128);
+      }
+      for (int i = 0; i < kItems; ++i) {
+        bar_init(&ctl->item_full[i], 1);
+        bar_init(&ctl->item_empty[i], 1);
+        bar_init(&ctl->rows_full[i], 32);
+      }
+      bar_init(&ctl->fin, 1);
+      ctl->dead = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    tmem_alloc(&ctl->tmem, C::kTmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const int n_tiles = (int)c.left;
+  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
+  // An item's entry.  It is written again for item it + 16, once the epilogue is through with this
+  // one; all others have read it by then.
+  auto item_at = [&](uint32_t it) -> const Item& {
+    wait(&ctl->item_full[it % kItems], (it / kItems) & 1);
+    return ctl->item[it % kItems];
+  };
+
+  // 128 registers at launch: the softmax warps, which hold scores and sums of all rows,
+  // take from the others (208 + 96 + 112 + 96 = 4 * 128)
+  if (warp >= 4 && warp < 12) {
+    if (warp < 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    }
+    if (warp < 8) {
+      // -------------------------------------------------------------- loaders
+      constexpr int LPR = C::kRow / 16, RPI = 32 / LPR;  // lanes per row, rows per pass
+      const int lw = warp - 4, jl = lane / LPR, cl = lane % LPR, key = lw * 32 + lane;
+      const unsigned char* const base = reinterpret_cast<const unsigned char*>(P.pool) + cl * 16;
+      const uint32_t vstep = (uint32_t)(P.H * P.pt);
+      // places of this lane's chunks: the swizzle has NSW patterns
+      constexpr int NSW = RPI >= 8 ? 1 : 8 / RPI;
+      uint32_t swz[NSW];
+#pragma unroll
+      for (int k = 0; k < NSW; ++k) swz[k] = place<W>(kTK, k * RPI + jl, cl) - k * RPI * W;
+      uint32_t it = 0;
+      int left = 0, j = 0, lo = 0, hi = 0, b = 0, off = 0;  // the item whose tiles are looked up
+      int pg[3], at[3], sq[3];  // page and place in it (-1: no such key) of this lane's key, three tiles
+      auto fetch = [&](int i, int ti) {
+        at[i] = -1;
+        pg[i] = 0;
+        if (ti < n_tiles) {
+          if (left == 0) {
+            const Item& x = item_at(it++);
+            left = x.n_tiles;
+            j = x.tile * kTK + key;
+            lo = x.lo;
+            hi = x.hi;
+            b = x.b;
+            off = x.h * P.pt;
+          }
+          if (j >= lo && j < hi) {
+            const int blk = kv_block(P, j);
+            pg[i] = __ldg(P.blocks + (int64_t)b * P.ldb + blk);
+            at[i] = off + (j - blk * P.pt);
+          }
+          sq[i] = b;
+          j += kTK;
+          --left;
+        }
+      };
+      fetch(0, 0);
+      fetch(1, 1);
+      uint32_t slot = 0, phase = 1;
+#pragma unroll 1
+      for (int ti = 0; ti < n_tiles; ++ti) {
+        fetch(2, ti + 2);
+        uint32_t row = kNoRow;
+        if (at[0] >= 0) {
+          if (pg[0] >= 0 && pg[0] < P.n_pages) row = ((uint32_t)pg[0] << P.row_shift) + (uint32_t)at[0];
+          else record_error(P.err, kErrKvPage, sq[0]);
+        }
+        const unsigned have = __ballot_sync(FULL_MASK, row != kNoRow);
+        uint32_t rows[32 / RPI];  // of this lane's chunks
+#pragma unroll
+        for (int k = 0; k < 32 / RPI; ++k) rows[k] = __shfl_sync(FULL_MASK, row, k * RPI + jl);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          wait(&ctl->kv_empty[slot], phase);
+          const uint32_t dst = sb + slot * C::kSlot + lw * 32 * W;
+          const unsigned char* const from = base + (part ? (int64_t)vstep * C::kRow : 0);
+          if (have == FULL_MASK) {
+#pragma unroll
+            for (int k = 0; k < 32 / RPI; ++k)
+              cp16(dst + k * RPI * W + swz[k % NSW], from + (uint64_t)rows[k] * C::kRow);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32 / RPI; ++k) {
+              const bool real = (have >> (k * RPI + jl)) & 1;
+              cp16(dst + k * RPI * W + swz[k % NSW], real ? from + (uint64_t)rows[k] * C::kRow : base, real);
+            }
+          }
+          if (part == 1) {
+            if (F8) {
+              const uint32_t sc = sb + C::kOffScale + ((ti % kMeta) * 2 * kTK + key) * 4;
+              const bool real = row != kNoRow;
+              cp4(sc, kv_scale(P, real ? row : 0), real);
+              cp4(sc + kTK * 4, kv_scale(P, real ? row + vstep : 0), real);
+            }
+            if (lane == 0) ctl->mask[ti % kMeta][lw] = have;
+          }
+          arrive_copies(&ctl->kv_full[slot]);
+          if (lane == 0) arrive(&ctl->kv_full[slot]);
+          if (++slot == S) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          pg[i] = pg[i + 1];
+          at[i] = at[i + 1];
+          sq[i] = sq[i + 1];
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 9) {
+      // ------------------------------------------------------ the run's items
+      if (lane == 0) {
+        for (uint32_t it = 0;; ++it) {
+          const int n = (int)min((long long)(c.x.t1 - c.tile), c.left);
+          Item x;
+          x.b = c.b;
+          x.h = c.h;
+          x.rt = c.rt;
+          x.R = min(c.s.n * A.G - c.rt * TM, TM);
+          x.row0 = c.s.row0;
+          x.first = c.s.len - c.s.n;
+          x.lo = c.x.lo;
+          x.hi = c.x.hi;
+          x.tile = c.tile;
+          x.n_tiles = n;
+          const bool starts = c.tile == c.x.t0, ends = c.tile + n == c.x.t1;
+          x.flags = (starts ? 1 : 0) | (ends ? 2 : 0) | (c.left == n ? 4 : 0);
+          x.pad = 0;
+          if (starts && !ends)
+            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.x.t1 - c.tile), total, ctas);
+          wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
+          ctl->item[it % kItems] = x;
+          arrive(&ctl->item_full[it % kItems]);
+          c.tile += n - 1;
+          c.left -= n - 1;
+          if (!c.next(A, cls)) break;
+        }
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ----------------------------------------------------- q, positions
+#pragma unroll 1
+      for (uint32_t it = 0;; ++it) {
+        const Item& x = item_at(it);
+        const int R = x.R, r_item = x.rt * TM, row0 = x.row0, hq0 = x.h * A.G, last = x.flags & 4;
+        const uint32_t dst = sb + C::kOffQ + (it & 1) * C::kQ;
+        for (int r = lane; r < C::kRows16; r += 32)
+          ctl->pos[it % kItems][r] = r < R ? x.first + (r_item + r) / A.G : -1;
+        wait(&ctl->q_empty[it & 1], ((it >> 1) & 1) ^ 1);
+        auto row_of = [&](int r) -> const uint16_t* {
+          const int t = (r_item + r) / A.G;
+          return A.q + (int64_t)(row0 + t) * A.ldq + (int64_t)(hq0 + (r_item + r) - t * A.G) * D;
+        };
+        const int rows = (R + 15) / 16 * 16;
+        if (!F8) {
+          constexpr int QL = D / 8, QR = 32 / QL;  // lanes per row, rows per pass
+          for (int r = lane / QL; r < rows; r += QR)
+            cp16(dst + place<128>(C::kQRows, r, lane % QL), r < R ? row_of(r) + (lane % QL) * 8 : A.q, r < R);
+        } else {
+          constexpr int QL = D / 4, QR = 32 / QL;  // four elements a lane
+          const int e0 = (lane % QL) * 4;
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += 4 * QR) {
+            uint2 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + k * QR + lane / QL;
+              v[k] = r < R ? __ldg(reinterpret_cast<const uint2*>(row_of(r) + e0)) : make_uint2(0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + k * QR + lane / QL;
+              float f[4];
+              up2<DT>(v[k].x, f[0], f[1]);
+              up2<DT>(v[k].y, f[2], f[3]);
+              uint32_t top = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+#pragma unroll
+              for (int o = QL / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+              const int e = min(max((int)(top >> 23) - 127, -100), 127);
+              const float up = __int_as_float((134 - e) << 23);  // 2^(7 - e)
+              uint32_t p[3] = {0, 0, 0};
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                // an infinity or a NaN becomes a NaN code (satfinite would make the infinity a number)
+                const float a = f[i] * up, b = f[i + 1] * up;
+                uint32_t h[3];
+                split3(a - a == 0.f ? a : NAN, b - b == 0.f ? b : NAN, h[0], h[1], h[2]);
+#pragma unroll
+                for (int q = 0; q < 3; ++q) p[q] |= h[q] << (8 * i);
+              }
+              const int col = r / 16 * 48 + r % 16;
+#pragma unroll
+              for (int q = 0; q < 3; ++q)
+                st_shared4(dst + place<W>(C::kQRows, col + q * 16, (lane % QL) >> 2) + (lane & 3) * 4, p[q]);
+              if (lane % QL == 0) ctl->qmul[it % kItems][r] = A.c * __int_as_float((120 + e) << 23);
+            }
+          }
+          fence_async_smem();
+        }
+        arrive_copies(&ctl->q_full[it & 1]);
+        arrive(&ctl->q_full[it & 1]);
+        arrive(&ctl->rows_full[it % kItems]);
+        if (last) break;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 8) {
+      // ---------------------------------------------------------- MMA issuer
+      {
+        const uint32_t fmt = !F8 && DT == SLORA_BF16 ? 1u : 0u;
+        // fp32 accumulators; K is K-major, V (bit 15) and the weights (bit 16) are MN-major
+        const uint32_t id_s = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
+        const uint32_t id_o = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) | (((uint32_t)D >> 4) << 24);
+        const uint32_t rows_hi = desc_hi(8 * W, W == 128 ? kSwizzle128 : kSwizzle64), weights_hi = desc_hi(kTK * 16, kNoSwizzle);
+        const uint32_t k_lo = desc_lo(sb, 16), q_lo = desc_lo(sb + C::kOffQ, 16), v_lo = desc_lo(sb, C::kPanel);
+        const uint32_t p_lo = desc_lo(sb + C::kOffP, 128);
+        uint32_t qslot = 0, qphase = 0, qit = 0, vslot = 1, vphase = 0, vit = 0, obuf = 0;
+        int qleft = 0, vleft = 0, qn = 0, vn = 0;
+        bool first = true;
+#pragma unroll 1
+        for (int step = 0; step <= n_tiles; ++step) {
+          if (step < n_tiles) {  // scores of tile `step`
+            const int ti = step;
+            if (qleft == 0) {
+              const Item& x = item_at(qit);
+              qleft = x.n_tiles;
+              qn = (x.R + 15) / 16;
+              wait(&ctl->q_full[qit & 1], (qit >> 1) & 1);
+            }
+            wait(&ctl->kv_full[qslot], qphase);
+            fence_async_smem();  // the copies were generic writes
+            tc_fence_after();
+            const uint32_t id = id_s | (uint32_t)(F8 ? qn * 6 : qn * 2) << 17;
+            const uint32_t a = k_lo + qslot * (C::kSlot >> 4), b = q_lo + (qit & 1) * (C::kQ >> 4);
+            const uint32_t d = tmem + (ti & 1) * C::kSCols;
+            --qleft;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < C::kRow / 32; ++k)
+                mma<F8>(d, a + (((k >> 2) * C::kPanel + (k & 3) * 32) >> 4), rows_hi,
+                        b + (((k >> 2) * (C::kQRows * W) + (k & 3) * 32) >> 4), rows_hi, id, k > 0);
+              mma_commit(&ctl->s_full[ti & 1]);
+              mma_commit(&ctl->kv_empty[qslot]);
+              if (qleft == 0) mma_commit(&ctl->q_empty[qit & 1]);
+            }
+            __syncwarp();
+            if (qleft == 0) ++qit;
+            qslot += 2;
+            if (qslot >= S) {
+              qslot -= S;
+              qphase ^= 1;
+            }
+          }
+          if (step > 0) {  // products of tile `step - 1`
+            const int ti = step - 1;
+            if (vleft == 0) {
+              const Item& x = item_at(vit++);
+              vleft = x.n_tiles;
+              vn = F8 ? (x.R + 15) / 16 * 6 : (x.R + 7) / 8 * 2;
+              first = true;
+              obuf = (vit - 1) % C::kOBufs;
+              wait(&ctl->o_empty[obuf], (((vit - 1) / C::kOBufs) & 1) ^ 1);
+            }
+            wait(&ctl->kv_full[vslot], vphase);
+            wait(&ctl->p_full[ti & 1], (ti >> 1) & 1);
+            fence_async_smem();
+            tc_fence_after();
+            const uint32_t id = id_o | (uint32_t)vn << 17;
+            const uint32_t a = v_lo + vslot * (C::kSlot >> 4), b = p_lo + (ti & 1) * (C::kP >> 4);
+            const uint32_t od = tmem + 2 * C::kSCols + obuf * C::kPCols;
+            --vleft;
+            constexpr int KK = F8 ? 32 : 16;  // keys per MMA
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kTK / KK; ++k)
+                mma<F8>(od, a + ((k * KK * W) >> 4), rows_hi, b + ((k * KK * 16) >> 4), weights_hi, id,
+                        !(first && k == 0));
+              mma_commit(&ctl->pv_done[ti & 1]);
+              mma_commit(&ctl->kv_empty[vslot]);
+              if (vleft == 0) mma_commit(&ctl->o_full[obuf]);
+            }
+            __syncwarp();
+            first = false;
+            vslot += 2;
+            if (vslot >= S) {
+              vslot -= S;
+              vphase ^= 1;
+            }
+          }
+        }
+        if (elect_one()) mma_commit(&ctl->fin);  // every product and arrival is done before the block ends
+        __syncwarp();
+        wait(&ctl->fin, 0);
+      }
+    }
+  } else if (warp < 4) {
+    // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    constexpr int HM = TM / 8;
+    const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16);
+    const float* const scales = reinterpret_cast<const float*>(smem + C::kOffScale);
+    uint32_t ti = 0, vslot = 1, vphase = 0;
+    float l[TM];  // this key's sums
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
+      const Item& x_ = item_at(it);
+      const int n_here = x_.n_tiles, tile0 = x_.tile, R = x_.R, flags = x_.flags;
+      const int NH = TM == 8 ? 1 : (R + 7) / 8;
+      const uint32_t to = ts + 2 * C::kSCols + it % C::kOBufs * C::kPCols;
+      wait(&ctl->rows_full[it % kItems], (it / kItems) & 1);
+      const int* const pos = ctl->pos[it % kItems];
+      const float* const qmul = ctl->qmul[it % kItems];
+      const int pmin = pos[0], pmax = pos[R - 1];
+      float vn = 0.f;
+#pragma unroll
+      for (int r = 0; r < TM; ++r) l[r] = 0.f;
+      if (tid < TM) ctl->ref[tid] = -INFINITY;
+      softmax_sync();
+#pragma unroll 1
+      for (int n = 0; n < n_here; ++n, ++ti) {
+        const uint32_t sbuf = ts + (ti & 1) * C::kSCols;
+        wait(&ctl->kv_full[vslot], vphase);  // scales and mask
+        wait(&ctl->s_full[ti & 1], (ti >> 1) & 1);
+        vslot += 2;
+        if (vslot >= S) {
+          vslot -= S;
+          vphase ^= 1;
+        }
+        tc_fence_after();
+        const uint32_t have = ctl->mask[ti % kMeta][warp];
+        float ks = 1.f, vs = 1.f;
+        if (F8) {
+          ks = scales[(ti % kMeta) * 2 * kTK + tid];
+          vs = scales[((ti % kMeta) * 2 + 1) * kTK + tid];
+        }
+        const int key0 = (tile0 + n) * kTK, j = key0 + tid;
+        const bool open = have == FULL_MASK && key0 + kTK - 1 <= pmin && (A.window <= 0 || key0 > pmax - A.window);
+        const bool mine = (have >> lane) & 1;
+        float s[TM];
+        bool over = F8 && mine && vs > vn;
+#pragma unroll
+        for (int h = 0; h < HM; ++h) {
+          if (h < NH) {
+            float* const x = s + h * 8;
+            if (!F8) {
+              ld8(sbuf + h * 8, x);
+              wait_ld8(x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] *= A.c;
+            } else {
+              const uint32_t col = sbuf + h / 2 * 48 + (h & 1) * 8;
+              float y[8], z[8];
+              ld8(col, x);
+              ld8(col + 16, y);
+              ld8(col + 32, z);
+              wait_ld8(x);
+              wait_ld8(y);
+              wait_ld8(z);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, x[i])) * (ks * qmul[h * 8 + i]);
+            }
+            if (!open) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int p = pos[h * 8 + i];
+                if (!mine || j > p || (A.window > 0 && j <= p - A.window)) x[i] = -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) over |= x[i] > ctl->ref[h * 8 + i] + kSlack;
+          }
+        }
+        if (softmax_any(over)) {  // some reference moves: to the tile's maxima
+#pragma unroll
+          for (int r = 0; r < TM; ++r)
+            if (r < NH * 8) {
+              const float v = warp_max(s[r]);
+              if (lane == 0) ctl->red[warp][r] = v;
+            }
+          if (F8) {
+            const float v = warp_max(mine ? vs : 0.f);
+            if (lane == 0) ctl->red[warp][TM] = v;
+          }
+          softmax_sync();
+          float ratio = 1.f;
+          if (F8) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v = fmaxf(v, ctl->red[w][TM]);
+            if (v > vn) {
+              v = fmaxf(2.f * v, 0x1p-126f);
+              ratio = vn / v;
+              vn = v;
+            }
+          }
+          if (tid < NH * 8) {
+            const int r = tid;
+            const float top = fmaxf(fmaxf(ctl->red[0][r], ctl->red[1][r]), fmaxf(ctl->red[2][r], ctl->red[3][r]));
+            const float m = ctl->ref[r], m1 = top > m + kSlack ? top : m;
+            ctl->fac[r] = m1 == m ? 1.f : ex2(m - m1);
+            ctl->ref[r] = m1;
+          }
+          if (n > 0) {  // the products so far
+            wait(&ctl->pv_done[(ti - 1) & 1], ((ti - 1) >> 1) & 1);
+            tc_fence_after();
+          }
+          softmax_sync();
+#pragma unroll
+          for (int h = 0; h < HM; ++h) {
+            if (h < NH) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) l[h * 8 + i] *= ctl->fac[h * 8 + i];
+            }
+          }
+          if (n > 0) {
+#pragma unroll 1
+            for (int h = 0; h < NH; ++h) {
+#pragma unroll 1
+              for (int q = 0; q < (F8 ? 3 : 2); ++q) {
+                const uint32_t col = to + (F8 ? h / 2 * 48 + q * 16 + (h & 1) * 8 : h * 16 + q * 8);
+                float o[8];
+                ld8(col, o);
+                wait_ld8(o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] *= ctl->fac[h * 8 + i] * ratio;
+                st8(col, o);
+              }
+            }
+          }
+          wait_st();
+        }
+        // the weights of tile ti - 2 have been used: its products were issued before these scores
+        const uint32_t pd = sb + C::kOffP + (ti & 1) * C::kP + tid * 16;
+        // relative V scale (a NaN scale of an unseen key stays out)
+        const float f = F8 ? vs * __frcp_rn(fmaxf(vn, 0x1p-126f)) * kLift : kLift;
+        uint32_t q8[3][4];
+#pragma unroll
+        for (int h = 0; h < (HM + 1) / 2 * 2; ++h) {
+          if (h < NH || (F8 && (h & 1) && h < NH + 1)) {
+            uint32_t w[3][4] = {};
+            if (h < HM && h < NH) {
+              float p[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = h < HM ? h * 8 + i : 0;
+                const float m = ctl->ref[r];
+                p[i] = ex2(s[r] - (m == -INFINITY ? 0.f : m));
+                l[r] += p[i];
+                if (F8) p[i] = s[r] == -INFINITY ? 0.f : p[i] * f;
+                else p[i] *= f;
+              }
+              if (!F8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split2<DT>(p[2 * i], p[2 * i + 1], w[0][i], w[1][i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = p[i] <= 448.f ? p[i] : NAN;  // never above, but an infinite scale
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split3(p[2 * i], p[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+              }
+            }
+            if (!F8) {
+              st_shared16(pd + (2 * h) * (kTK * 16), w[0][0], w[0][1], w[0][2], w[0][3]);
+              st_shared16(pd + (2 * h + 1) * (kTK * 16), w[1][0], w[1][1], w[1][2], w[1][3]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 3; ++q) {
+                q8[q][(h & 1) * 2] = w[q][0] | w[q][1] << 16;
+                q8[q][(h & 1) * 2 + 1] = w[q][2] | w[q][3] << 16;
+                if (h & 1) st_shared16(pd + (h / 2 * 3 + q) * (kTK * 16), q8[q][0], q8[q][1], q8[q][2], q8[q][3]);
+              }
+            }
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        arrive(&ctl->p_full[ti & 1]);
+      }
+
+      // ---- the item's sums, for the epilogue (which is through with those of item it - 2)
+      wait(&ctl->o_empty[it % C::kOBufs], ((it / C::kOBufs) & 1) ^ 1);
+#pragma unroll
+      for (int h = 0; h < HM; ++h) {
+        if (h < NH) {  // over the warp's keys: lane i * 4 ends with row i of the eight
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = l[h * 8 + i];
+#pragma unroll
+          for (int st = 0; st < 3; ++st) {
+            const int o = 16 >> st, half = 4 >> st;
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+              const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+              v[i] = keep + __shfl_xor_sync(FULL_MASK, give, o);
+            }
+          }
+          v[0] += __shfl_xor_sync(FULL_MASK, v[0], 2);
+          v[0] += __shfl_xor_sync(FULL_MASK, v[0], 1);
+          if ((lane & 3) == 0) ctl->sum[it & 1][warp][h * 8 + (lane >> 2)] = v[0];
+        }
+      }
+      if (tid < TM) ctl->end_ref[it & 1][tid] = ctl->ref[tid];
+      if (tid == 0) ctl->unit[it & 1] = (F8 ? vn : 1.f) * (1.f / kLift);
+      arrive(&ctl->sum_full[it & 1]);
+      if (flags & 4) break;
+    }
+  } else {
+    // ------------------------------------------- the rows of an item, or their partials
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    const int wl = warp - 12, tl = tid - 384;
+    const uint32_t ts = tmem + ((uint32_t)(wl * 32) << 16);
+    const int d = D == 128 ? tl : wl * 16 + (lane & 15);
+    const bool writes = D == 128 || lane < 16;
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
+      const Item& x_ = item_at(it);
+      const int R = x_.R, flags = x_.flags, r_item = x_.rt * TM, hq0 = x_.h * A.G;
+      const int NH = (R + 7) / 8;
+      const int64_t row0 = x_.row0;
+      const bool complete = (flags & 3) == 3;
+      float* const part = parts + (size_t)(2 * blockIdx.x + (it > 0 ? 1 : 0)) * slot_floats(TM, D);
+      const uint32_t to = ts + 2 * C::kSCols + it % C::kOBufs * C::kPCols;
+      wait(&ctl->sum_full[it & 1], (it >> 1) & 1);
+      if (tl < R) {
+        const int r = tl, t = (r_item + r) / A.G, hq = hq0 + (r_item + r) - t * A.G;
+        const float (*const sum)[TM] = ctl->sum[it & 1];
+        const float m = ctl->end_ref[it & 1][r], lr = (sum[0][r] + sum[1][r]) + (sum[2][r] + sum[3][r]);
+        ctl->out_fac[r] = complete ? inverse(lr) : lr == 0.f ? 0.f : 1.f;
+        if (complete) {
+          if (A.lse) A.lse[(row0 + t) * A.Hq + hq] = lse_of(m, lr);
+        } else {
+          part[(size_t)TM * D + r] = m;
+          part[(size_t)TM * (D + 1) + r] = lr;
+        }
+      }
+      const float unit = ctl->unit[it & 1];
+      epilogue_sync();
+      wait(&ctl->o_full[it % C::kOBufs], (it / C::kOBufs) & 1);
+      tc_fence_after();
+      uint32_t bad[2] = {0, 0};
+#pragma unroll 1
+      for (int h = 0; h < NH; ++h) {
+        float o[8], y[8], z[8];
+        const uint32_t col = to + (F8 ? h / 2 * 48 + (h & 1) * 8 : h * 16);
+        ld8(col, o);
+        ld8(col + (F8 ? 16 : 8), y);
+        if (F8) ld8(col + 32, z);
+        wait_ld8(o);
+        wait_ld8(y);
+        if (F8) wait_ld8(z);
+        int t = (r_item + h * 8) / A.G, hq = r_item + h * 8 - t * A.G;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = h * 8 + i;
+          if (r < R) {
+            const float fr = ctl->out_fac[r];
+            float v = (F8 ? fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, o[i])) : o[i] + y[i]) * unit;
+            if (fr == 0.f) v = 0.f;  // sees no key
+            if (writes) {
+              if (!(fabsf(v) < INFINITY)) bad[r >> 5] |= 1u << (r & 31);
+              if (complete) A.out[(row0 + t) * A.ldo + (int64_t)(hq0 + hq) * D + d] = (uint16_t)pk2<DT>(v * fr, 0.f);
+              else part[(size_t)r * D + d] = v;
+            }
+          }
+          if (++hq == A.G) {
+            hq = 0;
+            ++t;
+          }
+        }
+      }
+      tc_fence_before();
+      const bool spoiled = epilogue_any((bad[0] | bad[1]) != 0);
+      if (spoiled) {
+        // rows that are not finite: once more without the keys that they do not see
+        bad[0] = __reduce_or_sync(FULL_MASK, bad[0]);
+        bad[1] = __reduce_or_sync(FULL_MASK, bad[1]);
+        if (lane == 0) {
+          ctl->bad[wl][0] = bad[0];
+          ctl->bad[wl][1] = bad[1];
+        }
+        epilogue_sync();
+#pragma unroll 1
+        for (int r = wl; r < R; r += 4) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) any |= ctl->bad[w][r >> 5];
+          if (!((any >> (r & 31)) & 1) || ctl->end_ref[it & 1][r] == -INFINITY) continue;
+          const int t = (r_item + r) / A.G, hq = hq0 + (r_item + r) - t * A.G;
+          redo_row<DT, FMT, D>(A, x_.b, x_.h, A.q + (row0 + t) * A.ldq + (int64_t)hq * D, x_.first + t,
+                               max(x_.tile * kTK, x_.lo), min((x_.tile + x_.n_tiles) * kTK, x_.hi), ctl->end_ref[it & 1][r],
+                               ctl->out_fac[r], complete ? A.out + (row0 + t) * A.ldo + (int64_t)hq * D : nullptr,
+                               part + (size_t)r * D);
+        }
+        epilogue_sync();
+      }
+      arrive(&ctl->o_empty[it % C::kOBufs]);
+      if (tl == 0) arrive(&ctl->item_empty[it % kItems]);
+      if (flags & 4) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, C::kTmem);
+}
+
+template <int DT, int FMT, int D, int TM>
+cudaError_t run_decode(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream_t st) {
+  using C = Cfg<FMT, D, TM>;
+  constexpr int bytes = 1024 + C::kOffCtl + (int)sizeof(Ctl<TM, C::kSlots>);
+  static_assert(bytes <= 232448, "shared memory");
+  static std::atomic<bool> sized[64];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_decode<DT, FMT, D, TM>), bytes, sized);
+  if (e != cudaSuccess) return e;
+  k_kv_decode<DT, FMT, D, TM><<<sm_count, kNT, bytes, st>>>(A, cls);
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 != cudaSuccess ? e2 : launch_combine<DT, D, TM>(A, sm_count, st);
+}
+
+constexpr int max_rows_of(int fmt) { return fmt == SLORA_KV_16 ? 32 : 48; }
+
+// Row tiles as high as the call's largest sequence needs: the code for 8 rows is a fraction
+// of that for 48, and its ring is deeper.
+template <int DT, int FMT, int D>
+cudaError_t run_rows(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream_t st) {
+  const int64_t rows = (int64_t)A.G * A.max_rows;
+  if (rows <= 8) return run_decode<DT, FMT, D, 8>(A, sm_count, cls, st);
+  if (rows <= 16) return run_decode<DT, FMT, D, 16>(A, sm_count, cls, st);
+  return run_decode<DT, FMT, D, max_rows_of(FMT)>(A, sm_count, cls, st);
+}
+
+}  // namespace
+
+size_t kv_stream_workspace(int fmt, int D, int sm_count) {
+  return (size_t)sm_count * sizeof(Split) + 2 * (size_t)sm_count * slot_floats(max_rows_of(fmt), D) * 4;
+}
+
+cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s) {
+  const RowClass cls = {0, row_limit};
+  if (D == 128) {
+    if (dtype == SLORA_F16)
+      return fmt == SLORA_KV_16 ? run_rows<SLORA_F16, SLORA_KV_16, 128>(A, sm_count, cls, s)
+                                : run_rows<SLORA_F16, SLORA_KV_E4M3, 128>(A, sm_count, cls, s);
+    return fmt == SLORA_KV_16 ? run_rows<SLORA_BF16, SLORA_KV_16, 128>(A, sm_count, cls, s)
+                              : run_rows<SLORA_BF16, SLORA_KV_E4M3, 128>(A, sm_count, cls, s);
+  }
+  if (dtype == SLORA_F16)
+    return fmt == SLORA_KV_16 ? run_rows<SLORA_F16, SLORA_KV_16, 64>(A, sm_count, cls, s)
+                              : run_rows<SLORA_F16, SLORA_KV_E4M3, 64>(A, sm_count, cls, s);
+  return fmt == SLORA_KV_16 ? run_rows<SLORA_BF16, SLORA_KV_16, 64>(A, sm_count, cls, s)
+                            : run_rows<SLORA_BF16, SLORA_KV_E4M3, 64>(A, sm_count, cls, s);
+}
+
+}  // namespace slora

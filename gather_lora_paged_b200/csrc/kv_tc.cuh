@@ -1,0 +1,97 @@
+// kv_tc.cuh -- tensor-core helpers of the attention kernels (kv_decode.cu,
+// kv_chunk.cu), beside those of tc_common.cuh.
+//
+// MMAs are issued by a converged warp through elect.sync, with descriptors whose upper words are
+// constants and whose lower words grow by constants: an M = 128, N = 128, K = 16
+// product then issues every 69 cycles (64 are its work); from a branch on the lane number, with the
+// descriptors put together for each, it was 142.
+#pragma once
+
+#include "tc_common.cuh"
+
+namespace slora {
+namespace {
+
+using namespace tc;
+
+__device__ __forceinline__ void arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
+}
+// An arrival when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_copies(uint64_t* b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+template <bool F8>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                    uint32_t acc) {
+  if (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A from TMEM, 16-bit operands.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// The two words of a shared-memory descriptor (tc_common.cuh has the layouts).
+__device__ __forceinline__ constexpr uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return addr >> 4 | lbo >> 4 << 16; }
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
+  return sbo >> 4 | 1u << 14 | swizzle << 29;
+}
+constexpr uint32_t kNoSwizzle = 0, kSwizzle128 = 2, kSwizzle64 = 4;
+// The slow part of a wait: bounded, and over at once when another one gave up.
+__device__ __forceinline__ void wait_slow(uint64_t* b, uint32_t parity, int* dead, int32_t* err) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(su32(b)), "r"(parity) : "memory");
+    if (done || *reinterpret_cast<volatile int*>(dead)) return;
+    if (clock64() - t0 > kWaitLimitS) {
+      rec_err(err, 5, (int)blockIdx.x);
+      *reinterpret_cast<volatile int*>(dead) = 1;
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ void wait_for(uint64_t* b, uint32_t parity, int* dead, int32_t* err) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done) : "r"(su32(b)), "r"(parity) : "memory");
+  if (!done) wait_slow(b, parity, dead, err);
+}
+
+}  // namespace
+}  // namespace slora

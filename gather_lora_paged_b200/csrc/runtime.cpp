@@ -1172,7 +1172,13 @@ static slora_status_t kv_plan(slora_pool* P, const slora_kv_layout_t* L, const i
     return P->fail(SLORA_ERR_UNSUPPORTED, "the pool holds 2^32 rows of head_dim values or more");
   K.n_pages = (int)P->d.n_pages;
   K.H = L->n_kv_heads;
+  if (pt > (1ll << 30)) return P->fail(SLORA_ERR_UNSUPPORTED, "a page holds more than 2^30 tokens");
   K.pt = (int)pt;
+  // with 2^bits >= pt, pt_mul * pt exceeds 2^(30 + bits) by less than pt: exact below 2^30
+  int bits = 0;
+  while ((1ll << bits) < K.pt) ++bits;
+  K.pt_shift = 30 + bits;
+  K.pt_mul = (uint32_t)(((1ull << K.pt_shift) + K.pt - 1) / K.pt);
   K.scale_off = (int)(2 * (int64_t)L->n_kv_heads * pt * L->head_dim / 4);
   K.row_start = row_start;
   K.kv_len = kv_len;
@@ -1273,7 +1279,7 @@ size_t slora_kv_attention_workspace_bytes(const slora_pool* P, const slora_kv_la
                                           int32_t B, int32_t T, int32_t max_rows) {
   if (!P || !kv_layout_ok(layout) || n_q_heads < 1 || n_q_heads % layout->n_kv_heads || B < 1 || T < 1 || max_rows < 1)
     return 0;
-  const size_t stream = kv_stream_workspace(layout->head_dim, P->sm_count);
+  const size_t stream = kv_stream_workspace(layout->format, layout->head_dim, P->sm_count);
   return kv_has_chunks(n_q_heads / layout->n_kv_heads, std::min(max_rows, T))
              ? std::max(stream, kv_chunk_workspace(layout->head_dim, P->sm_count))
              : stream;

@@ -164,6 +164,8 @@ struct KvDev {
   int n_pages;
   int H;                     // kv heads
   int pt;                    // tokens per page
+  uint32_t pt_mul;           // position / pt = position * pt_mul >> pt_shift (positions are below 2^30)
+  int pt_shift;
   int scale_off;             // e4m3: floats from a page's start to its scales
   const int32_t* row_start;  // [B + 1]
   const int32_t* kv_len;     // [B]
@@ -190,10 +192,10 @@ cudaError_t launch_kv_write(const KvDev& P, int dtype, int fmt, int D, const voi
                             int64_t ldv, int sm_count, cudaStream_t s);
 cudaError_t launch_kv_read(const KvDev& P, int dtype, int fmt, int D, void* k, int64_t ldk, void* v, int64_t ldv,
                            int sm_count, cudaStream_t s);
-// Sequences of at most row_limit rows per kv head (kv_attention.cu), and of more (kv_chunk.cu).
+// Sequences of at most row_limit rows per kv head (kv_decode.cu), and of more (kv_chunk.cu).
 constexpr int kKvStreamRows = 64;
 cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s);
-size_t kv_stream_workspace(int D, int sm_count);
+size_t kv_stream_workspace(int fmt, int D, int sm_count);
 cudaError_t launch_kv_chunk(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s);
 size_t kv_chunk_workspace(int D, int sm_count);
 
