@@ -32,6 +32,11 @@ inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<bool>* do
 
 constexpr float kLn2 = 0.69314718055994531f;
 
+// Token of a row of a kv head.
+__device__ __forceinline__ int token_of(const KvAttnDev& A, int row) {
+  return (int)(((uint64_t)(uint32_t)row * A.g_mul) >> A.g_shift);
+}
+
 // The sequences a kernel takes: those with row_lo < rows per kv head <= row_hi.
 struct RowClass {
   int lo, hi;
@@ -183,6 +188,34 @@ __device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int m
   return true;
 }
 
+// What a run has to do, one entry per item, written by one warp for the others.
+struct Item {
+  int b, h, rt, R;        // sequence, kv head, row tile, rows
+  int row0, first;        // the sequence's first row and that row's position
+  int lo, hi;             // keys some row sees
+  int tile, n_tiles;      // this run's tiles of the item
+  int flags;              // 1: it starts here, 2: it ends here, 4: the run's last
+  int pad;
+};
+
+template <int TM, int TK>
+__device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK>& c) {
+  Item x;
+  x.b = c.b;
+  x.h = c.h;
+  x.rt = c.rt;
+  x.R = min(c.s.n * A.G - c.rt * TM, TM);
+  x.row0 = c.s.row0;
+  x.first = c.s.len - c.s.n;
+  x.lo = c.x.lo;
+  x.hi = c.x.hi;
+  x.tile = c.tile;
+  x.n_tiles = (int)min((long long)(c.x.t1 - c.tile), c.left);
+  x.flags = (c.tile == c.x.t0 ? 1 : 0) | (c.tile + x.n_tiles == c.x.t1 ? 2 : 0) | (c.left == x.n_tiles ? 4 : 0);
+  x.pad = 0;
+  return x;
+}
+
 // Partials of an item whose first tile is in this run (slot: this CTA's) and
 // whose last tile is number end - 1 of the line.
 __device__ __forceinline__ void note_split(Split* sp, int b, int h, int rt, int slot, long long end, long long total,
@@ -314,7 +347,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_kv_combine(KvAttnDev A) {
       }
     }
     const float inv = inverse(l);
-    const int t = (r_item + r) / A.G, hq = sp.h * A.G + (r_item + r) - t * A.G;
+    const int t = token_of(A, r_item + r), hq = sp.h * A.G + (r_item + r) - t * A.G;
     const int64_t tok = s.row0 + t;
     uint16_t* const orow = A.out + tok * A.ldo + (int64_t)hq * D + lane * E;
     if (E == 4)

@@ -27,20 +27,17 @@
 #include <math.h>
 
 #include "kv_attn.cuh"
-#include "tc_common.cuh"
+#include "kv_tc.cuh"
 
 namespace slora {
 namespace {
 
-using namespace tc;
-
-constexpr int kNT = 384;
+constexpr int kNT = 512;
 constexpr int kTM = 256;      // rows per item
 constexpr int kTK = 128;      // keys per tile
-constexpr int kLoadWarps = 3;
-constexpr int kLoaders = kLoadWarps * 32;
 constexpr int kMinRun = 2;
-constexpr int kCtlBytes = 1280;
+constexpr int kItems = 4;     // items that are known ahead
+constexpr int kMeta = 8;      // tiles whose scales and masks are kept
 constexpr float kSlack = 8.f; // log2 of the largest weight
 
 template <int FMT, int D>
@@ -51,51 +48,38 @@ struct Cfg {
   static constexpr int kQ = 2 * kSlot;                     // two q tiles
   static constexpr int kOffRing = kQ;
   static constexpr int kOffScale = kOffRing + kSlots * kSlot;
-  static constexpr int kScale = FMT == SLORA_KV_E4M3 ? 4 * 2 * kTK * 4 : 0;  // 4 tiles of K and V scales
-  static constexpr int kOffQs = kOffScale + kScale;        // score multipliers of the 256 rows
-  static constexpr int kOffCtl = kOffQs + (FMT == SLORA_KV_E4M3 ? 2 * kTM * 4 : 0);  // of two items
-  static constexpr int kSmem = 1024 + kOffCtl + kCtlBytes;
-  static_assert(kSmem <= 232448, "shared memory");
+  static constexpr int kScale = FMT == SLORA_KV_E4M3 ? kMeta * 2 * kTK * 4 : 0;  // K and V scales of tiles
+  static constexpr int kOffQs = kOffScale + kScale;        // score multipliers of items' rows
+  static constexpr int kOffCtl = kOffQs + (FMT == SLORA_KV_E4M3 ? kItems * kTM * 4 : 0);
 };
 
+template <int S>
 struct Ctl {
-  uint64_t kv_full[5], kv_empty[5], q_full, q_empty, s_full[2], p_full[2], o_full[2], fin;
+  uint64_t kv_full[S], kv_empty[S], q_full, q_empty, item_full[kItems], item_empty[kItems], rows_full[kItems];
+  uint64_t s_full[2], p_full[2], o_full[2], fin;
+  Item item[kItems];
   uint32_t tmem;
-  int dead;                          // a wait gave up: nobody waits any more
-  uint32_t any_bad[4][4];            // [tile & 3][loader warp]: keys on bad pages
-  uint32_t bad[4][kLoadWarps][4];    // their bits
-  float vtop[4][4];                  // [tile & 3][loader warp]: largest V scale
-  uint32_t rows[kLoadWarps][64];     // the loader warps' pool rows of a tile
+  int dead;                    // a wait gave up: nobody waits any more
+  uint32_t mask[kMeta][4];     // keys of a tile that are there
 };
-static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
-__device__ __forceinline__ void arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ bool ready(uint64_t* b, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done) : "r"(su32(b)), "r"(parity) : "memory");
-  return done;
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-// Products with the A operand in TMEM.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
@@ -127,8 +111,23 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* u) {
       "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
 }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// tcgen05.wait::ld, tied to the registers that a load fills
+__device__ __forceinline__ void wait_ld32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // Byte offset of 16-byte chunk c (8 elements) of row j in a slot: panels of 64
 // elements, 128-byte rows, chunks swizzled by the row.
@@ -139,12 +138,14 @@ __device__ __forceinline__ uint32_t place(int j, int c) {
 template <int DT, int FMT, int D>
 __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvAttnDev A, RowClass cls) {
   using C = Cfg<FMT, D>;
-  constexpr int MT = FMT == SLORA_KV_16 ? DT : SLORA_F16;  // operand type of the products
+  constexpr bool F8 = FMT == SLORA_KV_E4M3;
+  constexpr int MT = F8 ? SLORA_F16 : DT;  // operand type of the products
   constexpr int S = C::kSlots;
+  using Control = Ctl<S>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = su32(smem);
-  Ctl* const ctl = reinterpret_cast<Ctl*>(smem + C::kOffCtl);
+  Control* const ctl = reinterpret_cast<Control*>(smem + C::kOffCtl);
   float* const scales = reinterpret_cast<float*>(smem + C::kOffScale);
   float* const qscale = reinterpret_cast<float*>(smem + C::kOffQs);
   const KvDev& P = A.kv;
@@ -152,20 +153,26 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   Split* const split = reinterpret_cast<Split*>(A.workspace) + blockIdx.x;
   float* const parts = reinterpret_cast<float*>(reinterpret_cast<Split*>(A.workspace) + gridDim.x);
 
+  griddep_launch();  // the join's CTAs may take their places (they wait for this grid's end)
   if (tid == 0) split->n = 0;
   Cursor<kTM, kTK> c;
   long long total, u1;
   int ctas;
   if (!find_run<kTM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) return;
 
-  if (warp == 11) {
+  if (warp == 12) {
     if (lane == 0) {
       for (int i = 0; i < S; ++i) {
-        bar_init(&ctl->kv_full[i], kLoaders);
+        bar_init(&ctl->kv_full[i], 128 + (F8 ? 128 : 4));
         bar_init(&ctl->kv_empty[i], 1);
       }
-      bar_init(&ctl->q_full, kLoaders);
+      bar_init(&ctl->q_full, 256);
       bar_init(&ctl->q_empty, 1);
+      for (int i = 0; i < kItems; ++i) {
+        bar_init(&ctl->item_full[i], 1);
+        bar_init(&ctl->item_empty[i], 2);
+        bar_init(&ctl->rows_full[i], 128);
+      }
       for (int i = 0; i < 2; ++i) {
         bar_init(&ctl->s_full[i], 1);
         bar_init(&ctl->p_full[i], 128);
@@ -182,110 +189,163 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (*reinterpret_cast<volatile int*>(&ctl->dead)) return;
-    if (!bar_wait(b, parity, P.err)) *reinterpret_cast<volatile int*>(&ctl->dead) = 1;
+  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
+  // An item's entry.  It is written again for item it + 4, once both softmax groups are through with
+  // this one; all others have read it by then.
+  auto item_at = [&](uint32_t it) -> const Item& {
+    wait(&ctl->item_full[it % kItems], (it / kItems) & 1);
+    return ctl->item[it % kItems];
   };
 
-  // 168 registers at launch: the softmax warps, which hold a row's scores, take
-  // from the others (104 * 128 + 200 * 256 = 136 * 128 + 184 * 256 = 168 * 384)
-  if (warp >= 8) {
-    if (FMT == SLORA_KV_16) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
-  if (warp < 11) {
-    // ---------------------------------------------------------------- loaders
-    const int lw = warp - 8;
-    constexpr int LPR = C::kSlot ? (FMT == SLORA_KV_16 ? D / 8 : D / 16) : 1;  // lanes per cached row (16 bytes each)
-    constexpr int RPI = 32 / LPR;
-    constexpr int KW = (kTK + kLoadWarps - 1) / kLoadWarps;                    // keys per warp: lw, lw + 3, ...
-    constexpr int KM = (KW + RPI - 1) / RPI;                                   // passes over them
-    const int jl = lane / LPR, cl = lane % LPR;
-    uint32_t* const rows_of = ctl->rows[lw];
-    const unsigned char* const base = reinterpret_cast<const unsigned char*>(P.pool);
-    const uint32_t vstep = (uint32_t)(P.H * P.pt);
-    uint32_t g = 0, qi = 0, ti = 0;        // slots, items and tiles so far
-    uint64_t *pend0 = nullptr, *pend1 = nullptr;  // barriers of copies in flight, oldest first
-    auto flush = [&] {
-      if (pend0 || pend1) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        fence_async_smem();
-        if (pend0) arrive(pend0);
-        if (pend1) arrive(pend1);
-        pend0 = pend1 = nullptr;
-      }
-    };
-    auto push = [&](uint64_t* b) {
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (pend0) {
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-        fence_async_smem();
-        arrive(pend0);
-      }
-      pend0 = pend1;
-      pend1 = b;
-    };
-    auto acquire = [&](uint64_t* b, uint32_t parity) {  // what is in flight may be what the slot waits for
-      if (!ready(b, parity)) {
-        flush();
-        wait(b, parity);
-      }
-    };
-    for (;;) {
-      const int n_tiles = (int)min((long long)(c.x.t1 - c.tile), c.left);
-      const int r_item = c.rt * kTM, R = min(c.s.n * A.G - r_item, kTM);
-      int pg[2];                              // pages of keys lw + 3 * lane and 32 keys of this warp on
-      auto fetch = [&](int tile) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int x = lw + kLoadWarps * (lane + 32 * q), j = tile * kTK + x;
-          pg[q] = x < kTK && j >= c.x.lo && j < c.x.hi ? __ldg(P.blocks + (int64_t)c.b * P.ldb + kv_block(P, j)) : 0;
+  // 128 registers at launch: the softmax warps, which hold a row's scores, take from the
+  // others (184 + 184 + 88 + 56 = 4 * 128)
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 13) {
+      // ------------------------------------------------------ the run's items
+      if (lane == 0) {
+        for (uint32_t it = 0;; ++it) {
+          const Item x = item_of(A, c);
+          if ((x.flags & 3) == 1)
+            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.x.t1 - c.tile), total, ctas);
+          wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
+          ctl->item[it % kItems] = x;
+          arrive(&ctl->item_full[it % kItems]);
+          c.tile += x.n_tiles - 1;
+          c.left -= x.n_tiles - 1;
+          if (!c.next(A, cls)) break;
         }
-      };
-      auto resolve = [&](int tile, uint32_t t) {  // the tile's rows from pg; t: its number
-        unsigned bad = 0;
-        __syncwarp();                             // the last tile's rows have been read
+      }
+      __syncwarp();
+    } else if (warp == 12) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t fmt = MT == SLORA_BF16 ? 1u : 0u;
+      const uint32_t id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
+      const uint32_t id_s = id0 | ((uint32_t)kTK >> 3) << 17, id_o = id0 | (1u << 16) | ((uint32_t)D >> 3) << 17;  // V: MN-major
+      const uint32_t hi = desc_hi(1024, kSwizzle128);
+      const uint32_t q_lo = desc_lo(sb, 16), k_lo = desc_lo(sb + C::kOffRing, 16), v_lo = desc_lo(sb + C::kOffRing, C::kPanel);
+      uint32_t g = 0, pn = 0;  // slots so far, tiles so far
+      uint32_t pn1 = 0;        // of the second q tile
+      auto qk = [&](int i, uint32_t slot) {
+        const uint32_t a = q_lo + i * (C::kSlot >> 4), b = k_lo + slot * (C::kSlot >> 4);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int x = lw + kLoadWarps * (lane + 32 * q), j = tile * kTK + x;
-          uint32_t r = kNoRow;
-          if (x < kTK && j >= c.x.lo && j < c.x.hi) {
-            if (pg[q] >= 0 && pg[q] < P.n_pages) r = ((uint32_t)pg[q] << P.row_shift) + (uint32_t)(c.h * P.pt + j - kv_block(P, j) * P.pt);
-            else bad |= 1u << q;
-          }
-          rows_of[lane + 32 * q] = r;
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * C::kPanel + (k & 3) * 32) >> 4;
+          mma<false>(tmem + i * 128, a + off, hi, b + off, hi, id_s, k > 0);
+        }
+        mma_commit(&ctl->s_full[i]);
+      };
+      auto pv = [&](int i, uint32_t slot, bool first) {
+        const uint32_t b = v_lo + slot * (C::kSlot >> 4);
+#pragma unroll
+        for (int k = 0; k < kTK / 16; ++k)
+          mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b + ((k * 2048) >> 4), hi, id_o, !(first && k == 0));
+      };
+#pragma unroll 1
+      for (uint32_t it = 0;; ++it) {
+        const Item& x = item_at(it);
+        const int n_tiles = x.n_tiles, last = x.flags & 4;
+        const bool two = x.R > 128;
+        wait(&ctl->q_full, it & 1);
+        wait(&ctl->kv_full[g % S], (g / S) & 1);
+        fence_async_smem();
+        tc_fence_after();
+        if (elect_one()) {
+          qk(0, g % S);
+          if (two) qk(1, g % S);
+          mma_commit(&ctl->kv_empty[g % S]);
+          if (n_tiles == 1) mma_commit(&ctl->q_empty);
         }
         __syncwarp();
-        const bool any = __any_sync(FULL_MASK, bad);
-        if (lane == 0) ctl->any_bad[t & 3][lw] = any;
-        if (any) {
-          if (lane == 0) record_error(P.err, kErrKvPage, c.b);
-          if (lane < 4) ctl->bad[t & 3][lw][lane] = 0;
-          __syncwarp();
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int x = lw + kLoadWarps * (lane + 32 * q);
-            if ((bad >> q) & 1) atomicOr(&ctl->bad[t & 3][lw][x >> 5], 1u << (x & 31));
+#pragma unroll 1
+        for (int n = 0; n < n_tiles; ++n, g += 2) {
+          const bool more = n + 1 < n_tiles;
+          const uint32_t v = (g + 1) % S, k = (g + 2) % S;
+          wait(&ctl->kv_full[v], ((g + 1) / S) & 1);
+          wait(&ctl->p_full[0], pn++ & 1);
+          fence_async_smem();
+          tc_fence_after();
+          if (elect_one()) {
+            pv(0, v, n == 0);
+            if (!more) mma_commit(&ctl->o_full[0]);
           }
+          __syncwarp();
+          if (more) {
+            wait(&ctl->kv_full[k], ((g + 2) / S) & 1);
+            fence_async_smem();
+            tc_fence_after();
+            if (elect_one()) qk(0, k);
+            __syncwarp();
+          }
+          if (two) {
+            wait(&ctl->p_full[1], pn1++ & 1);
+            tc_fence_after();
+          }
+          if (elect_one()) {
+            if (two) {
+              pv(1, v, n == 0);
+              if (!more) mma_commit(&ctl->o_full[1]);
+            }
+            mma_commit(&ctl->kv_empty[v]);
+            if (more) {
+              if (two) qk(1, k);
+              mma_commit(&ctl->kv_empty[k]);
+              if (n + 2 == n_tiles) mma_commit(&ctl->q_empty);
+            }
+          }
+          __syncwarp();
         }
+        if (last) break;
+      }
+      if (elect_one()) mma_commit(&ctl->fin);  // every product and arrival is done before the block ends
+      __syncwarp();
+      wait(&ctl->fin, 0);
+    }
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- loaders
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    constexpr int CB = F8 ? D : 2 * D;                         // bytes of a cached row
+    constexpr int LPR = CB / 16, RPI = 32 / LPR, KM = 32 / RPI;  // lanes per row, rows per pass, passes
+    const int lw = warp - 8, jl = lane / LPR, cl = lane % LPR, key = lw * 32 + lane;
+    const unsigned char* const base = reinterpret_cast<const unsigned char*>(P.pool) + cl * 16;
+    const uint32_t vstep = (uint32_t)(P.H * P.pt);
+    uint32_t g = 0, ti = 0;              // slots and tiles so far
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
+      const Item& x = item_at(it);
+      const int n_tiles = x.n_tiles, lo = x.lo, hi = x.hi, b = x.b, off = x.h * P.pt, last = x.flags & 4;
+      int j = x.tile * kTK + key;
+      const int32_t* const table = P.blocks + (int64_t)b * P.ldb;
+      int pg = 0, at = -1;                 // page and place in it (-1: no such key) of this lane's key in the next tile
+      auto fetch = [&] {
+        at = -1;
+        if (j >= lo && j < hi) {
+          const int blk = kv_block(P, j);
+          pg = __ldg(table + blk);
+          at = off + (j - blk * P.pt);
+        }
+        j += kTK;
       };
-      fetch(c.tile);
+      fetch();
 
       // q: rows of both tiles, zeros behind the item's last row
-      acquire(&ctl->q_empty, (qi & 1) ^ 1);
+      wait(&ctl->q_empty, (it & 1) ^ 1);
       {
         constexpr int QL = D / 8, QR = 32 / QL;  // lanes per row, rows per pass
+        const int R = x.R, r_item = x.rt * kTM, row0 = x.row0, hq0 = x.h * A.G;
         const int rows = R > 128 ? 256 : 128;
-        for (int p = lw; p < rows / QR; p += kLoadWarps) {
+#pragma unroll 2
+        for (int p = lw; p < rows / QR; p += 4) {
           const int r = p * QR + lane / QL, ch = lane % QL;
           const bool real = r < R;
-          const int t = real ? (r_item + r) / A.G : 0;
-          const uint16_t* src = A.q + (int64_t)(c.s.row0 + t) * A.ldq +
-                                (real ? (int64_t)(c.h * A.G + (r_item + r) - t * A.G) * D + ch * 8 : 0);
+          const int t = real ? token_of(A, r_item + r) : 0;
+          const uint16_t* src = A.q + (real ? (int64_t)(row0 + t) * A.ldq + (int64_t)(hq0 + (r_item + r) - t * A.G) * D + ch * 8 : 0);
           const uint32_t dst = sb + (r >> 7) * C::kSlot + place(r & 127, ch);
-          if (FMT == SLORA_KV_16 || DT == SLORA_F16) {
+          if (!F8 || DT == SLORA_F16) {
             cp16(dst, src, real);
-            if (FMT == SLORA_KV_E4M3 && ch == 0) qscale[(qi & 1) * kTM + r] = A.c;
-          } else {  // a bf16 row as fp16 times a power of two (see kv_decode.cu)
+            if (F8 && ch == 0) qscale[(it % kItems) * kTM + r] = A.c;
+          } else {  // a bf16 row as fp16 times a power of two: [1, 2) at its largest; what falls below fp16's
+                    // range is under 2^-25 of that
             const uint4 v = real ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t top = 0;
@@ -300,198 +360,144 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
             for (int i = 0; i < 4; ++i)
               h[i] = pack2<SLORA_F16>(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
             st_shared16(dst, h[0], h[1], h[2], h[3]);
-            if (ch == 0) qscale[(qi & 1) * kTM + r] = A.c * __int_as_float((127 + e) << 23);
+            if (ch == 0) qscale[(it % kItems) * kTM + r] = A.c * __int_as_float((127 + e) << 23);
           }
         }
+        if (F8) fence_async_smem();
       }
-      push(&ctl->q_full);
-      ++qi;
+      arrive_copies(&ctl->q_full);
+      arrive(&ctl->q_full);
+      arrive(&ctl->rows_full[it % kItems]);
 
-      if (FMT == SLORA_KV_16) {
+      auto resolve = [&](unsigned& have) -> uint32_t {  // the row of this lane's key
+        uint32_t row = kNoRow;
+        if (at >= 0) {
+          if (pg >= 0 && pg < P.n_pages) row = ((uint32_t)pg << P.row_shift) + (uint32_t)at;
+          else record_error(P.err, kErrKvPage, b);
+        }
+        have = __ballot_sync(FULL_MASK, row != kNoRow);
+        return row;
+      };
+      if (!F8) {
+#pragma unroll 1
         for (int n = 0; n < n_tiles; ++n, ++ti) {
-          resolve(c.tile + n, ti);
-          if (n + 1 < n_tiles) fetch(c.tile + n + 1);
+          unsigned have;
+          const uint32_t row = resolve(have);
+          if (n + 1 < n_tiles) fetch();
+          uint32_t rows[KM];  // of this lane's chunks
+#pragma unroll
+          for (int k = 0; k < KM; ++k) rows[k] = __shfl_sync(FULL_MASK, row, k * RPI + jl);
 #pragma unroll 1
           for (int part = 0; part < 2; ++part, ++g) {
-            acquire(&ctl->kv_empty[g % S], ((g / S) & 1) ^ 1);
+            wait(&ctl->kv_empty[g % S], ((g / S) & 1) ^ 1);
             const uint32_t slot = sb + C::kOffRing + (g % S) * C::kSlot;
-#pragma unroll 4
-            for (int k = 0; k < KM; ++k) {
-              const int x = lw + kLoadWarps * (k * RPI + jl);
-              const uint32_t r = rows_of[k * RPI + jl];
-              const int64_t at = r != kNoRow ? (int64_t)(r + part * vstep) * (2 * D) + cl * 16 : 0;
-              if (x < kTK) cp16(slot + place(x, cl), base + at, r != kNoRow);
+            const unsigned char* const from = base + (part ? (int64_t)vstep * CB : 0);
+            if (have == FULL_MASK) {
+#pragma unroll
+              for (int k = 0; k < KM; ++k) cp16(slot + place(lw * 32 + k * RPI + jl, cl), from + (uint64_t)rows[k] * CB);
+            } else {
+#pragma unroll
+              for (int k = 0; k < KM; ++k) {
+                const bool real = (have >> (k * RPI + jl)) & 1;
+                cp16(slot + place(lw * 32 + k * RPI + jl, cl), real ? from + (uint64_t)rows[k] * CB : base, real);
+              }
             }
-            push(&ctl->kv_full[g % S]);
+            if (part == 1 && lane == 0) ctl->mask[ti % kMeta][lw] = have;
+            arrive_copies(&ctl->kv_full[g % S]);
+            if (lane == 0) arrive(&ctl->kv_full[g % S]);
           }
         }
       } else {
-        uint4 code[2][KM];
-        auto load = [&](int part, uint32_t t) {  // codes to registers, scales straight to their place
+        uint4 code[KM];  // of the next slot
+        unsigned have = 0, have_next = 0;
+        uint32_t row = resolve(have);
+        auto load = [&](int part, uint32_t r0, unsigned hv) {
+          const unsigned char* const from = base + (part ? (int64_t)vstep * CB : 0);
 #pragma unroll
           for (int k = 0; k < KM; ++k) {
-            const int x = lw + kLoadWarps * (k * RPI + jl);
-            const uint32_t first_row = rows_of[k * RPI + jl];
-            const bool real = first_row != kNoRow;
-            const uint32_t r = real ? first_row + part * vstep : 0;
-            code[part][k] = make_uint4(0, 0, 0, 0);
-            if (real) code[part][k] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)r * D + cl * 16));
-            if (cl == 0 && x < kTK)
-              cp4(sb + C::kOffScale + (((t & 3) * 2 + part) * kTK + x) * 4, kv_scale(P, r), real);
+            const uint32_t r = __shfl_sync(FULL_MASK, r0, k * RPI + jl);
+            code[k] = make_uint4(0, 0, 0, 0);
+            if ((hv >> (k * RPI + jl)) & 1) code[k] = __ldg(reinterpret_cast<const uint4*>(from + (uint64_t)r * CB));
           }
         };
-        flush();
-        resolve(c.tile, ti);
-        if (n_tiles > 1) fetch(c.tile + 1);
-        load(0, ti);
-        load(1, ti);
+        load(0, row, have);
+#pragma unroll 1
         for (int n = 0; n < n_tiles; ++n, ++ti) {
+          uint32_t row_next = kNoRow;
 #pragma unroll
           for (int part = 0; part < 2; ++part, ++g) {
             wait(&ctl->kv_empty[g % S], ((g / S) & 1) ^ 1);
             const uint32_t slot = sb + C::kOffRing + (g % S) * C::kSlot;
-            if (part == 0) {  // the tile's scales have arrived: the largest of V's
-              asm volatile("cp.async.wait_all;" ::: "memory");
-              float top = 0.f;
-#pragma unroll
-              for (int k = 0; k < KM; ++k) {
-                const int x = lw + kLoadWarps * (k * RPI + jl);
-                if (cl == 0 && x < kTK) top = fmaxf(top, scales[((ti & 3) * 2 + 1) * kTK + x]);
-              }
-#pragma unroll
-              for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-              if (lane == 0) ctl->vtop[ti & 3][lw] = top;
-            }
 #pragma unroll
             for (int k = 0; k < KM; ++k) {
-              const int x = lw + kLoadWarps * (k * RPI + jl);
-              const uint32_t w[4] = {code[part][k].x, code[part][k].y, code[part][k].z, code[part][k].w};
-              if (x < kTK) {
+              const int y = lw * 32 + k * RPI + jl;
+              const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                  st_shared16(slot + place(x, 2 * cl + hh), e4m3x2_f16x2(w[2 * hh]), e4m3x2_f16x2(w[2 * hh] >> 16),
-                              e4m3x2_f16x2(w[2 * hh + 1]), e4m3x2_f16x2(w[2 * hh + 1] >> 16));
+              for (int hh = 0; hh < 2; ++hh)
+                st_shared16(slot + place(y, 2 * cl + hh), e4m3x2_f16x2(w[2 * hh]), e4m3x2_f16x2(w[2 * hh] >> 16),
+                            e4m3x2_f16x2(w[2 * hh + 1]), e4m3x2_f16x2(w[2 * hh + 1] >> 16));
+            }
+            if (part == 0) {
+              load(1, row, have);
+              if (n + 1 < n_tiles) fetch();
+            } else {
+              const uint32_t sc = sb + C::kOffScale + ((ti % kMeta) * 2 * kTK + key) * 4;
+              const bool real = row != kNoRow;
+              cp4(sc, kv_scale(P, real ? row : 0), real);
+              cp4(sc + kTK * 4, kv_scale(P, real ? row + vstep : 0), real);
+              if (lane == 0) ctl->mask[ti % kMeta][lw] = have;
+              if (n + 1 < n_tiles) {
+                row_next = resolve(have_next);
+                load(0, row_next, have_next);
               }
             }
             fence_async_smem();
+            arrive_copies(&ctl->kv_full[g % S]);
             arrive(&ctl->kv_full[g % S]);
-            if (n + 1 < n_tiles) {
-              // the next tile: K after this one's K, V after its V.  Its place among the scales and
-              // bad-page bits is that of tile ti - 3, which is through: K's slot of this tile was free
-              if (part == 0) {
-                resolve(c.tile + n + 1, ti + 1);
-                if (n + 2 < n_tiles) fetch(c.tile + n + 2);
-              }
-              load(part, ti + 1);
-            }
           }
+          row = row_next;
+          have = have_next;
         }
       }
-      c.tile += n_tiles - 1;
-      c.left -= n_tiles - 1;
-      if (!c.next(A, cls)) break;
+      if (last) break;
     }
-    flush();
-  } else {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t id_s = idesc_f16(MT, kTK, 0), id_o = idesc_f16(MT, D, 1);
-      const uint32_t ring = sb + C::kOffRing;
-      uint32_t g = 0, qi = 0, pn[2] = {0, 0};
-      auto qk = [&](int i, uint32_t slot) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * C::kPanel + (k & 3) * 32;
-          mma_f16(tmem + i * 128, sdesc(sb + i * C::kSlot + off, 16, 1024), sdesc(ring + slot * C::kSlot + off, 16, 1024), id_s,
-                  k > 0);
-        }
-        mma_commit(&ctl->s_full[i]);
-      };
-      auto pv = [&](int i, uint32_t slot, bool first) {
-        wait(&ctl->p_full[i], pn[i]++ & 1);
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < kTK / 16; ++k)
-          mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, sdesc(ring + slot * C::kSlot + k * 2048, C::kPanel, 1024),
-                     id_o, !(first && k == 0));
-      };
-      for (;;) {
-        const int n_tiles = (int)min((long long)(c.x.t1 - c.tile), c.left);
-        const bool two = c.s.n * A.G - c.rt * kTM > 128;
-        wait(&ctl->q_full, qi++ & 1);
-        wait(&ctl->kv_full[g % S], (g / S) & 1);
-        tc_fence_after();
-        qk(0, g % S);
-        if (two) qk(1, g % S);
-        mma_commit(&ctl->kv_empty[g % S]);
-        if (n_tiles == 1) mma_commit(&ctl->q_empty);
-        for (int n = 0; n < n_tiles; ++n, g += 2) {
-          const bool more = n + 1 < n_tiles;
-          const uint32_t v = (g + 1) % S, k = (g + 2) % S;
-          wait(&ctl->kv_full[v], ((g + 1) / S) & 1);
-          pv(0, v, n == 0);
-          if (!more) mma_commit(&ctl->o_full[0]);
-          if (more) {
-            wait(&ctl->kv_full[k], ((g + 2) / S) & 1);
-            tc_fence_after();
-            qk(0, k);
-          }
-          if (two) {
-            pv(1, v, n == 0);
-            if (!more) mma_commit(&ctl->o_full[1]);
-          }
-          mma_commit(&ctl->kv_empty[v]);
-          if (more) {
-            if (two) qk(1, k);
-            mma_commit(&ctl->kv_empty[k]);
-            if (n + 2 == n_tiles) mma_commit(&ctl->q_empty);
-          }
-        }
-        c.tile += n_tiles - 1;
-        c.left -= n_tiles - 1;
-        if (!c.next(A, cls)) break;
-      }
-      mma_commit(&ctl->fin);  // every product and every commit's arrival is done before the block ends
-      bar_wait(&ctl->fin, 0, P.err);
-    }
-    __syncwarp();
-  }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // -------------------------------------------------------------- softmax
-    if (FMT == SLORA_KV_16) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int wg = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + wg * 128, to = tmem + lanes + 256 + wg * 128;
     uint32_t sn = 0, on = 0, ti = 0;
-    int segs = 0;
-    for (;;) {
-      const int n_tiles = (int)min((long long)(c.x.t1 - c.tile), c.left);
-      const int r_item = c.rt * kTM, R = min(c.s.n * A.G - r_item, kTM);
-      const bool whole_end = c.tile + n_tiles == c.x.t1;
-      const bool complete = whole_end && c.tile == c.x.t0;
-      const int slot = 2 * blockIdx.x + (segs > 0 ? 1 : 0);
-      if (!whole_end && c.tile == c.x.t0 && tid == 0)
-        note_split(split, c.b, c.h, c.rt, slot, u1 - c.left + (c.x.t1 - c.tile), total, ctas);
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
+      const Item& x = item_at(it);
+      const int n_tiles = x.n_tiles, tile0 = x.tile, R = x.R, flags = x.flags, first = x.first, r_item = x.rt * kTM;
       if (wg == 0 || R > 128) {
         const int r = wg * 128 + (warp & 3) * 32 + lane;
-        const int first = c.s.len - c.s.n;
-        const int t = r < R ? (r_item + r) / A.G : 0;
+        const int t = r < R ? token_of(A, r_item + r) : 0;
         const int pos = r < R ? first + t : -1;
         const int low = A.window > 0 && r < R ? pos - A.window : -1;   // keys above it are seen
-        const int pmin = first + (r_item + wg * 128) / A.G;            // of the first row of this q tile
-        const int pmax = first + (r_item + R - 1) / A.G;
+        const int pmin = first + token_of(A, r_item + wg * 128);       // of the first row of this q tile
+        const int pmax = first + token_of(A, r_item + R - 1);
         float m = -INFINITY, l = 0.f, vn = 0.f, cr = A.c;
+        if (F8) {
+          wait(&ctl->rows_full[it % kItems], (it / kItems) & 1);
+          cr = qscale[(it % kItems) * kTM + r];
+        }
+#pragma unroll 1
         for (int n = 0; n < n_tiles; ++n, ++ti) {
+          const uint32_t g = 2 * ti + 1;
+          wait(&ctl->kv_full[g % S], (g / S) & 1);  // scales and mask
           wait(&ctl->s_full[wg], sn++ & 1);
           tc_fence_after();
           float s[kTK];
 #pragma unroll
           for (int i = 0; i < kTK; i += 32) ld32(ts + i, s + i);
-          if (FMT == SLORA_KV_E4M3 && n == 0) cr = qscale[(segs & 1) * kTM + r];
-          wait_ld();
-          if (FMT == SLORA_KV_E4M3) {
-            const float* ks = scales + (ti & 3) * 2 * kTK;
+#pragma unroll
+          for (int i = 0; i < kTK; i += 32) wait_ld32(s + i);
+          const float* const ks = scales + (ti % kMeta) * 2 * kTK;
+          if (F8) {
 #pragma unroll
             for (int i = 0; i < kTK; i += 4) {
               const float4 k4 = *reinterpret_cast<const float4*>(ks + i);
@@ -501,44 +507,40 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
               s[i + 3] *= k4.w;
             }
           }
-          const int key0 = (c.tile + n) * kTK;
-          const uint32_t any = ctl->any_bad[ti & 3][0] | ctl->any_bad[ti & 3][1] | ctl->any_bad[ti & 3][2];
-          const bool masked = key0 + kTK - 1 > pmin || (A.window > 0 && key0 <= pmax - A.window) || any;
+          const int key0 = (tile0 + n) * kTK;
+          const uint4 have = *reinterpret_cast<const uint4*>(ctl->mask[ti % kMeta]);
+          const bool masked = key0 + kTK - 1 > pmin || (A.window > 0 && key0 <= pmax - A.window) ||
+                              (have.x & have.y & have.z & have.w) != FULL_MASK;
           if (masked) {
             const int hi = pos - key0, lo = low - key0;
+            const uint32_t hv[4] = {have.x, have.y, have.z, have.w};
 #pragma unroll
-            for (int i = 0; i < kTK; ++i)
-              if (i > hi || i <= lo) s[i] = -INFINITY;
-            if (any) {
+            for (int w = 0; w < 4; ++w) {
+              // bits of the keys lo < i <= hi
+              const int h2 = min(max(hi - 32 * w + 1, 0), 32), l2 = min(max(lo - 32 * w + 1, 0), 32);
+              const uint32_t below_h = h2 == 32 ? FULL_MASK : (1u << h2) - 1, below_l = l2 == 32 ? FULL_MASK : (1u << l2) - 1;
+              const uint32_t seen = hv[w] & below_h & ~below_l;
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                uint32_t bits = 0;
-                for (int q = 0; q < kLoadWarps; ++q)
-                  if (ctl->any_bad[ti & 3][q]) bits |= ctl->bad[ti & 3][q][w];
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if ((bits >> i) & 1) s[w * 32 + i] = -INFINITY;
-              }
+              for (int i = 0; i < 32; ++i)
+                if (!((seen >> i) & 1)) s[w * 32 + i] = -INFINITY;
             }
           }
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kTK; i += 4) {
-            top[0] = fmaxf(top[0], s[i]);
-            top[1] = fmaxf(top[1], s[i + 1]);
-            top[2] = fmaxf(top[2], s[i + 2]);
-            top[3] = fmaxf(top[3], s[i + 3]);
+          for (int i = 0; i < kTK; i += 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top[q] = fmaxf(fmaxf(top[q], s[i + 2 * q]), s[i + 2 * q + 1]);
           }
           const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cr);
           float ratio = 1.f;
           bool raise = false;
-          if (FMT == SLORA_KV_E4M3) {
-            const float tv = fmaxf(fmaxf(ctl->vtop[ti & 3][0], ctl->vtop[ti & 3][1]), ctl->vtop[ti & 3][2]);
-            if (n == 0) {
-              vn = fmaxf(tv, 0x1p-126f);
-            } else if (tv > 8.f * vn) {
-              ratio = vn / tv;
-              vn = tv;
+          if (F8) {
+            const float4 v4 = *reinterpret_cast<const float4*>(ks + kTK + lane * 4);
+            const float tv = warp_max(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)));
+            if (tv > vn || n == 0) {
+              const float v = fmaxf(2.f * tv, 0x1p-126f);
+              ratio = vn / v;
+              vn = v;
               raise = true;
             }
           }
@@ -548,11 +550,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
             l *= a;
             if (n > 0) {
               const float f = a * ratio;
-#pragma unroll
+#pragma unroll 1
               for (int i = 0; i < D; i += 32) {
                 float o[32];
                 ld32(to + i, o);
-                wait_ld();
+                wait_ld32(o);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] *= f;
                 st32(to + i, o);
@@ -560,8 +562,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
             }
           }
           const float mz = m == -INFINITY ? 0.f : m;
-          const float vinv = FMT == SLORA_KV_E4M3 ? __frcp_rn(vn) : 1.f;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          const float vinv = F8 ? __frcp_rn(vn) : 1.f;
+          const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz);
+          uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int i = 0; i < kTK; i += 32) {
             uint32_t w[16];
@@ -569,12 +572,14 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
             for (int k = 0; k < 32; k += 4) {
               float p[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                p[q] = ex2(fmaf(s[i + k + q], cr, -mz));
-                ls[q] += p[q];
+              for (int q = 0; q < 4; q += 2) {
+                unpair(fma2(pair(s[i + k + q], s[i + k + q + 1]), c2, m2), p[q], p[q + 1]);
+                p[q] = ex2(p[q]);
+                p[q + 1] = ex2(p[q + 1]);
+                ls[(k >> 1 & 2) + (q >> 1)] = add2(ls[(k >> 1 & 2) + (q >> 1)], pair(p[q], p[q + 1]));
               }
-              if (FMT == SLORA_KV_E4M3) {
-                const float4 v4 = *reinterpret_cast<const float4*>(scales + (ti & 3) * 2 * kTK + kTK + i + k);
+              if (F8) {
+                const float4 v4 = *reinterpret_cast<const float4*>(ks + kTK + i + k);
                 const float f[4] = {v4.x * vinv, v4.y * vinv, v4.z * vinv, v4.w * vinv};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) p[q] = masked && p[q] == 0.f ? 0.f : p[q] * f[q];  // a NaN scale of an unseen key stays out
@@ -584,7 +589,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
             }
             st16(ts + i / 2, w);
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          {
+            float a, b;
+            unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), a, b);
+            l += a + b;
+          }
           wait_st();
           tc_fence_before();
           arrive(&ctl->p_full[wg]);
@@ -593,24 +602,26 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         // ---- the rows of this item, or their partials
         wait(&ctl->o_full[wg], on++ & 1);
         tc_fence_after();
-        const int hq = r < R ? c.h * A.G + (r_item + r) - t * A.G : 0;
-        const int64_t tok = c.s.row0 + t;
+        const bool complete = (flags & 3) == 3;
+        const int hq0 = x.h * A.G, hq = r < R ? hq0 + (r_item + r) - t * A.G : 0;
+        const int64_t row0 = x.row0, tok = row0 + t;
         const float inv = inverse(l);
         uint16_t* const orow = A.out + tok * A.ldo + (int64_t)hq * D;
-        float* const part = parts + (size_t)slot * slot_floats(kTM, D);
+        float* const part = parts + (size_t)(2 * blockIdx.x + (it > 0 ? 1 : 0)) * slot_floats(kTM, D);
         float* const prow = part + (size_t)r * D;
-        const float f = complete ? inv : 1.f;
+        const float f = (F8 ? vn : 1.f), f1 = complete ? inv : 1.f;
         bool bad = false;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           float o[32];
           ld32(to + i, o);
-          wait_ld();
+          wait_ld32(o);
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            if (FMT == SLORA_KV_E4M3) o[k] *= vn;
-            bad |= !isfinite(o[k]);
-            o[k] *= f;
+            if (F8) o[k] *= f;
+            if (l == 0.f) o[k] = 0.f;  // sees no key
+            bad |= !(fabsf(o[k]) < INFINITY);
+            o[k] *= f1;
           }
           if (r < R) {
             if (complete) {
@@ -635,40 +646,44 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           }
         }
         unsigned again = __ballot_sync(FULL_MASK, bad && r < R && m != -INFINITY);
+#pragma unroll 1
         while (again) {
           __syncwarp();
           const int src = __ffs(again) - 1;
           again &= again - 1;
           const int r2 = wg * 128 + (warp & 3) * 32 + src;
-          const int t2 = (r_item + r2) / A.G, hq2 = c.h * A.G + (r_item + r2) - t2 * A.G;
-          const int64_t tok2 = c.s.row0 + t2;
-          redo_row<DT, FMT, D>(A, c.b, c.h, A.q + tok2 * A.ldq + (int64_t)hq2 * D, first + t2,
-                               max(c.tile * kTK, c.x.lo), min((c.tile + n_tiles) * kTK, c.x.hi),
-                               __shfl_sync(FULL_MASK, m, src), __shfl_sync(FULL_MASK, inv, src),
+          const int t2 = token_of(A, r_item + r2), hq2 = hq0 + (r_item + r2) - t2 * A.G;
+          const int64_t tok2 = row0 + t2;
+          redo_row<DT, FMT, D>(A, x.b, x.h, A.q + tok2 * A.ldq + (int64_t)hq2 * D, first + t2, max(tile0 * kTK, x.lo),
+                               min((tile0 + n_tiles) * kTK, x.hi), __shfl_sync(FULL_MASK, m, src),
+                               __shfl_sync(FULL_MASK, inv, src),
                                complete ? A.out + tok2 * A.ldo + (int64_t)hq2 * D : nullptr, part + (size_t)r2 * D);
         }
       } else {
         ti += n_tiles;
       }
-      ++segs;
-      c.tile += n_tiles - 1;
-      c.left -= n_tiles - 1;
-      if (!c.next(A, cls)) break;
+      // all four warps are through with the entry
+      if (wg == 0) asm volatile("barrier.sync 1, 128;" ::: "memory");
+      else asm volatile("barrier.sync 2, 128;" ::: "memory");
+      if ((tid & 127) == 0) arrive(&ctl->item_empty[it % kItems]);
+      if (flags & 4) break;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 11) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
 template <int DT, int FMT, int D>
 cudaError_t run_chunk(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream_t st) {
   using C = Cfg<FMT, D>;
   static std::atomic<bool> sized[64];
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_chunk<DT, FMT, D>), C::kSmem, sized);
+  constexpr int bytes = 1024 + C::kOffCtl + (int)sizeof(Ctl<C::kSlots>);
+  static_assert(bytes <= 232448, "shared memory");
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_chunk<DT, FMT, D>), bytes, sized);
   if (e != cudaSuccess) return e;
-  k_kv_chunk<DT, FMT, D><<<sm_count, kNT, C::kSmem, st>>>(A, cls);
+  k_kv_chunk<DT, FMT, D><<<sm_count, kNT, bytes, st>>>(A, cls);
   const cudaError_t e2 = cudaGetLastError();
   return e2 != cudaSuccess ? e2 : launch_combine<DT, D, kTM>(A, sm_count, st);
 }

@@ -85,16 +85,6 @@ struct Cfg {
   static_assert(kTmemCols <= 512, "TMEM");
 };
 
-// What a run has to do, one entry per item, written by one warp for the others.
-struct Item {
-  int b, h, rt, R;        // sequence, kv head, row tile, rows
-  int row0, first;        // the sequence's first row and that row's position
-  int lo, hi;             // keys some row sees
-  int tile, n_tiles;      // this run's tiles of the item
-  int flags;              // 1: it starts here, 2: it ends here, 4: the run's last
-  int pad;
-};
-
 template <int TM, int S>
 struct Ctl {
   uint64_t kv_full[S], kv_empty[S], q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], rows_full[kItems];
@@ -113,9 +103,6 @@ struct Ctl {
   uint32_t bad[4][2];                         // warps' rows that are not finite
 };
 
-__device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 __device__ __forceinline__ void st_shared4(uint32_t dst, uint32_t a) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(a) : "memory");
 }
@@ -351,28 +338,14 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       // ------------------------------------------------------ the run's items
       if (lane == 0) {
         for (uint32_t it = 0;; ++it) {
-          const int n = (int)min((long long)(c.x.t1 - c.tile), c.left);
-          Item x;
-          x.b = c.b;
-          x.h = c.h;
-          x.rt = c.rt;
-          x.R = min(c.s.n * A.G - c.rt * TM, TM);
-          x.row0 = c.s.row0;
-          x.first = c.s.len - c.s.n;
-          x.lo = c.x.lo;
-          x.hi = c.x.hi;
-          x.tile = c.tile;
-          x.n_tiles = n;
-          const bool starts = c.tile == c.x.t0, ends = c.tile + n == c.x.t1;
-          x.flags = (starts ? 1 : 0) | (ends ? 2 : 0) | (c.left == n ? 4 : 0);
-          x.pad = 0;
-          if (starts && !ends)
+          const Item x = item_of(A, c);
+          if ((x.flags & 3) == 1)
             note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.x.t1 - c.tile), total, ctas);
           wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
           ctl->item[it % kItems] = x;
           arrive(&ctl->item_full[it % kItems]);
-          c.tile += n - 1;
-          c.left -= n - 1;
+          c.tile += x.n_tiles - 1;
+          c.left -= x.n_tiles - 1;
           if (!c.next(A, cls)) break;
         }
       }
@@ -385,10 +358,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         const int R = x.R, r_item = x.rt * TM, row0 = x.row0, hq0 = x.h * A.G, last = x.flags & 4;
         const uint32_t dst = sb + C::kOffQ + (it & 1) * C::kQ;
         for (int r = lane; r < C::kRows16; r += 32)
-          ctl->pos[it % kItems][r] = r < R ? x.first + (r_item + r) / A.G : -1;
+          ctl->pos[it % kItems][r] = r < R ? x.first + token_of(A, r_item + r) : -1;
         wait(&ctl->q_empty[it & 1], ((it >> 1) & 1) ^ 1);
         auto row_of = [&](int r) -> const uint16_t* {
-          const int t = (r_item + r) / A.G;
+          const int t = token_of(A, r_item + r);
           return A.q + (int64_t)(row0 + t) * A.ldq + (int64_t)(hq0 + (r_item + r) - t * A.G) * D;
         };
         const int rows = (R + 15) / 16 * 16;
@@ -764,7 +737,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       const uint32_t to = ts + 2 * C::kSCols + it % C::kOBufs * C::kPCols;
       wait(&ctl->sum_full[it & 1], (it >> 1) & 1);
       if (tl < R) {
-        const int r = tl, t = (r_item + r) / A.G, hq = hq0 + (r_item + r) - t * A.G;
+        const int r = tl, t = token_of(A, r_item + r), hq = hq0 + (r_item + r) - t * A.G;
         const float (*const sum)[TM] = ctl->sum[it & 1];
         const float m = ctl->end_ref[it & 1][r], lr = (sum[0][r] + sum[1][r]) + (sum[2][r] + sum[3][r]);
         ctl->out_fac[r] = complete ? inverse(lr) : lr == 0.f ? 0.f : 1.f;
@@ -790,7 +763,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         wait_ld8(o);
         wait_ld8(y);
         if (F8) wait_ld8(z);
-        int t = (r_item + h * 8) / A.G, hq = r_item + h * 8 - t * A.G;
+        int t = token_of(A, r_item + h * 8), hq = r_item + h * 8 - t * A.G;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = h * 8 + i;
@@ -827,7 +800,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 #pragma unroll
           for (int w = 0; w < 4; ++w) any |= ctl->bad[w][r >> 5];
           if (!((any >> (r & 31)) & 1) || ctl->end_ref[it & 1][r] == -INFINITY) continue;
-          const int t = (r_item + r) / A.G, hq = hq0 + (r_item + r) - t * A.G;
+          const int t = token_of(A, r_item + r), hq = hq0 + (r_item + r) - t * A.G;
           redo_row<DT, FMT, D>(A, x_.b, x_.h, A.q + (row0 + t) * A.ldq + (int64_t)hq * D, x_.first + t,
                                max(x_.tile * kTK, x_.lo), min((x_.tile + x_.n_tiles) * kTK, x_.hi), ctl->end_ref[it & 1][r],
                                ctl->out_fac[r], complete ? A.out + (row0 + t) * A.ldo + (int64_t)hq * D : nullptr,

@@ -1147,6 +1147,15 @@ int32_t slora_kv_page_tokens(const slora_pool* P, const slora_kv_layout_t* layou
   return (int32_t)std::min<int64_t>(kv_page_tokens_of(P, layout), INT32_MAX);
 }
 
+// n / d as n * mul >> shift for 0 <= n < 2^30, 1 <= d <= 2^30: with 2^bits >= d, mul * d exceeds
+// 2^(30 + bits) by less than d, so the product is off by less than 2^(30 + bits) / d.
+static void divide_by(int d, uint32_t& mul, int& shift) {
+  int bits = 0;
+  while ((1ll << bits) < d) ++bits;
+  shift = 30 + bits;
+  mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+}
+
 // The checks that all KV calls share; fills the kernels' view of the batch.
 static slora_status_t kv_plan(slora_pool* P, const slora_kv_layout_t* L, const int32_t* row_start, const int32_t* kv_len,
                               const int32_t* blocks, int64_t ldb, int32_t B, int32_t T, KvDev& K) {
@@ -1174,11 +1183,7 @@ static slora_status_t kv_plan(slora_pool* P, const slora_kv_layout_t* L, const i
   K.H = L->n_kv_heads;
   if (pt > (1ll << 30)) return P->fail(SLORA_ERR_UNSUPPORTED, "a page holds more than 2^30 tokens");
   K.pt = (int)pt;
-  // with 2^bits >= pt, pt_mul * pt exceeds 2^(30 + bits) by less than pt: exact below 2^30
-  int bits = 0;
-  while ((1ll << bits) < K.pt) ++bits;
-  K.pt_shift = 30 + bits;
-  K.pt_mul = (uint32_t)(((1ull << K.pt_shift) + K.pt - 1) / K.pt);
+  divide_by(K.pt, K.pt_mul, K.pt_shift);
   K.scale_off = (int)(2 * (int64_t)L->n_kv_heads * pt * L->head_dim / 4);
   K.row_start = row_start;
   K.kv_len = kv_len;
@@ -1316,6 +1321,9 @@ slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout
   A.lse = lse;
   A.Hq = n_q_heads;
   A.G = n_q_heads / layout->n_kv_heads;
+  if ((int64_t)A.G * std::min(max_rows, T) > (1ll << 30))
+    return P->fail(SLORA_ERR_UNSUPPORTED, "a sequence of 2^30 rows per kv head or more");
+  divide_by(A.G, A.g_mul, A.g_shift);
   A.c = (float)((double)scale * 1.4426950408889634);
   A.window = window;
   A.max_rows = std::min(max_rows, T);

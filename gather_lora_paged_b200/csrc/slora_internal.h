@@ -183,6 +183,8 @@ struct KvAttnDev {
   int64_t ldo;
   float* lse;                // [T][Hq], may be NULL
   int Hq, G;                 // query heads, query heads per kv head
+  uint32_t g_mul;            // row / G = row * g_mul >> g_shift (rows are below 2^30)
+  int g_shift;
   float c;                   // scale * log2(e)
   int window;                // 0: none
   int max_rows;
