@@ -297,23 +297,20 @@ __device__ __noinline__ void redo_row(const KvAttnDev& A, int b, int h, const ui
   }
 }
 
-// Joins the partials of the item that starts in run blockIdx.x and ends in a
+// Joins the partials of the item that starts in run `run` of a kernel's `ctas` and ends in a
 // later one: weights exp2(m_i - max m), in key order.  A warp per row.
 constexpr int kCombineThreads = 128;
 template <int DT, int D, int TM>
-__global__ void __launch_bounds__(kCombineThreads) k_kv_combine(KvAttnDev A) {
+__device__ __forceinline__ void join_item(const KvAttnDev& A, const void* workspace, int run, int ctas) {
   constexpr int E = D / 32;
-  griddep_wait();
-  const Split sp = reinterpret_cast<const Split*>(A.workspace)[blockIdx.x];
+  const Split sp = reinterpret_cast<const Split*>(workspace)[run];
   if (sp.n == 0) return;
-  const float* const parts = reinterpret_cast<const float*>(reinterpret_cast<const Split*>(A.workspace) + gridDim.x);
+  const float* const parts = reinterpret_cast<const float*>(reinterpret_cast<const Split*>(workspace) + ctas);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   KvSeq s;
   kv_seq(A.kv, sp.b, A.max_rows, s);
   const int r_item = sp.rt * TM, R = min(s.n * A.G - r_item, TM);
-  auto at = [&](int i) {
-    return parts + (size_t)(i == 0 ? sp.slot : 2 * ((int)blockIdx.x + i)) * slot_floats(TM, D);
-  };
+  auto at = [&](int i) { return parts + (size_t)(i == 0 ? sp.slot : 2 * (run + i)) * slot_floats(TM, D); };
   for (int r = blockIdx.y * 4 + warp; r < R; r += gridDim.y * 4) {
     float top = -INFINITY;
     for (int i = lane; i < sp.n; i += 32) top = fmaxf(top, at(i)[(size_t)TM * D + r]);
@@ -358,21 +355,22 @@ __global__ void __launch_bounds__(kCombineThreads) k_kv_combine(KvAttnDev A) {
   }
 }
 
-
-// Launches the join behind the kernel that writes the partials (a programmatic
-// dependent launch: its CTAs are in place when that kernel ends).
-template <int DT, int D, int TM>
-cudaError_t launch_combine(const KvAttnDev& A, int grid, cudaStream_t st) {
+// The kernels of a call follow one another by programmatic dependent launch: kv_chunk.cu's CTAs
+// start where those of kv_decode.cu end (it waits for that grid before it ends itself, as
+// nothing else would), and the join's are in place when the last of them ends.
+template <typename K, typename... Args>
+cudaError_t launch_behind(K kern, dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, TM >= 16 ? TM / 16 : 1);
-  cfg.blockDim = dim3(kCombineThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv_combine<DT, D, TM>, A);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-// kv_chunk.cu -- attention of prompt chunks (more than 64 rows per kv head) over
+// kv_chunk.cu -- attention of prompt chunks (more rows per kv head than kv_decode.cu takes) over
 // the KV pages on the 5th-generation tensor cores.  Definition and row order as
 // in kv_decode.cu; runs, partials and their join as in kv_attn.cuh.
 //
@@ -150,15 +150,18 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   float* const qscale = reinterpret_cast<float*>(smem + C::kOffQs);
   const KvDev& P = A.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Split* const split = reinterpret_cast<Split*>(A.workspace) + blockIdx.x;
-  float* const parts = reinterpret_cast<float*>(reinterpret_cast<Split*>(A.workspace) + gridDim.x);
+  Split* const split = reinterpret_cast<Split*>(A.chunk_workspace) + blockIdx.x;
+  float* const parts = reinterpret_cast<float*>(reinterpret_cast<Split*>(A.chunk_workspace) + gridDim.x);
 
   griddep_launch();  // the join's CTAs may take their places (they wait for this grid's end)
   if (tid == 0) split->n = 0;
   Cursor<kTM, kTK> c;
   long long total, u1;
   int ctas;
-  if (!find_run<kTM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) return;
+  if (!find_run<kTM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) {
+    griddep_wait();
+    return;
+  }
 
   if (warp == 12) {
     if (lane == 0) {
@@ -673,6 +676,15 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   __syncthreads();
   tc_fence_after();
   if (warp == 12) tmem_dealloc(tmem, 512);
+  griddep_wait();  // for kv_decode.cu's grid: who waits for this one waits for both
+}
+
+// The joins of kv_decode.cu's items (row tiles of TM) and, if there are two grids, of this file's.
+template <int DT, int D, int TM>
+__global__ void __launch_bounds__(kCombineThreads) k_kv_join(KvAttnDev A, int ctas) {
+  griddep_wait();
+  if ((int)blockIdx.x < ctas) join_item<DT, D, TM>(A, A.workspace, blockIdx.x, ctas);
+  else join_item<DT, D, kTM>(A, A.chunk_workspace, blockIdx.x - ctas, ctas);
 }
 
 template <int DT, int FMT, int D>
@@ -683,9 +695,16 @@ cudaError_t run_chunk(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream
   static_assert(bytes <= 232448, "shared memory");
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_chunk<DT, FMT, D>), bytes, sized);
   if (e != cudaSuccess) return e;
-  k_kv_chunk<DT, FMT, D><<<sm_count, kNT, bytes, st>>>(A, cls);
-  const cudaError_t e2 = cudaGetLastError();
-  return e2 != cudaSuccess ? e2 : launch_combine<DT, D, kTM>(A, sm_count, st);
+  return launch_behind(k_kv_chunk<DT, FMT, D>, dim3(sm_count), kNT, bytes, st, A, cls);
+}
+
+template <int DT, int D>
+cudaError_t run_join(const KvAttnDev& A, int TM, bool chunks, int sm_count, cudaStream_t st) {
+  const dim3 grid(chunks ? 2 * sm_count : sm_count, chunks ? kTM / 16 : (TM + 15) / 16);
+  if (TM == 8) return launch_behind(k_kv_join<DT, D, 8>, grid, kCombineThreads, 0, st, A, sm_count);
+  if (TM == 16) return launch_behind(k_kv_join<DT, D, 16>, grid, kCombineThreads, 0, st, A, sm_count);
+  if (TM == 32) return launch_behind(k_kv_join<DT, D, 32>, grid, kCombineThreads, 0, st, A, sm_count);
+  return launch_behind(k_kv_join<DT, D, 48>, grid, kCombineThreads, 0, st, A, sm_count);
 }
 
 }  // namespace
@@ -694,8 +713,16 @@ size_t kv_chunk_workspace(int D, int sm_count) {
   return (size_t)sm_count * sizeof(Split) + 2 * (size_t)sm_count * slot_floats(kTM, D) * 4;
 }
 
-cudaError_t launch_kv_chunk(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s) {
-  const RowClass cls = {row_limit, INT32_MAX};
+cudaError_t launch_kv_join(const KvAttnDev& A, int dtype, int D, int TM, bool chunks, int sm_count, cudaStream_t s) {
+  if (D == 128)
+    return dtype == SLORA_F16 ? run_join<SLORA_F16, 128>(A, TM, chunks, sm_count, s)
+                              : run_join<SLORA_BF16, 128>(A, TM, chunks, sm_count, s);
+  return dtype == SLORA_F16 ? run_join<SLORA_F16, 64>(A, TM, chunks, sm_count, s)
+                            : run_join<SLORA_BF16, 64>(A, TM, chunks, sm_count, s);
+}
+
+cudaError_t launch_kv_chunk(const KvAttnDev& A, int dtype, int fmt, int D, int sm_count, cudaStream_t s) {
+  const RowClass cls = {kv_stream_rows(fmt), INT32_MAX};
   if (D == 128) {
     if (dtype == SLORA_F16)
       return fmt == SLORA_KV_16 ? run_chunk<SLORA_F16, SLORA_KV_16, 128>(A, sm_count, cls, s)

@@ -16,15 +16,15 @@
 // no thread touches a cached element, and the rows only fill N, a multiple of 16.
 // Items, runs, partials and their join: kv_attn.cuh.
 //
-// One CTA per SM, 16 warps:
-//   warps 4..7  copy K and V rows into a ring of slots (K or V of a tile), 32 keys
+// One CTA per SM, 20 warps:
+//   warps 8..11 copy K and V rows into a ring of slots (K or V of a tile), 32 keys
 //               each; the copies signal the slot's barrier when they land;
-//   warp 9      the run's items, for all others;
-//   warp 10     q of the items ahead, as the N side of S^T, and the rows' positions;
-//   warp 8      issues S^T of tile i + 1, then O^T of tile i;
-//   warps 0..3  the softmax: a thread owns a key, reads its scores from TMEM and
-//               writes its weights to shared memory as the N side of O^T;
-//   warps 12..15  an item's end: O^T from TMEM to the output, beside the next item.
+//   warp 13     the run's items, for all others;
+//   warp 14     q of the items ahead, as the N side of S^T, and the rows' positions;
+//   warp 12     issues S^T of tile i + 1, then O^T of tile i;
+//   warps 0..7  the softmax: a thread owns a key and half of the rows, reads its scores from TMEM
+//               and writes its weights to shared memory as the N side of O^T;
+//   warps 16..19  an item's end: O^T from TMEM to the output, beside the next item.
 //
 // Weights are exp(s - m) with m a former maximum of the row: it moves (and O^T is
 // scaled) only when a score exceeds it by 2^3, which one vote per tile finds out.
@@ -50,7 +50,7 @@
 namespace slora {
 namespace {
 
-constexpr int kNT = 512;       // threads
+constexpr int kNT = 640;       // threads
 constexpr int kTK = 128;       // keys per tile
 constexpr int kMinRun = 1;     // tiles that are worth a CTA of their own
 constexpr int kMeta = 8;       // tiles whose scales and masks are kept: what the ring holds, at least
@@ -103,6 +103,9 @@ struct Ctl {
   uint32_t bad[4][2];                         // warps' rows that are not finite
 };
 
+__device__ __forceinline__ void st_shared8(uint32_t dst, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ void st_shared4(uint32_t dst, uint32_t a) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(a) : "memory");
 }
@@ -111,6 +114,17 @@ __device__ __forceinline__ void ld8(uint32_t taddr, float* v) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
                : "r"(taddr));
+}
+__device__ __forceinline__ void ld4(uint32_t taddr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(taddr));
+}
+__device__ __forceinline__ void st4(uint32_t taddr, const float* v) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+               "r"(u[3])
+               : "memory");
 }
 __device__ __forceinline__ void st8(uint32_t taddr, const float* v) {
   const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
@@ -125,22 +139,40 @@ __device__ __forceinline__ void wait_ld8(float* v) {
                :
                : "memory");
 }
+__device__ __forceinline__ void wait_ld4(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]) : : "memory");
+}
+template <int N>
+__device__ __forceinline__ void ld_n(uint32_t taddr, float* v) {
+  if (N == 8) ld8(taddr, v);
+  else ld4(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void st_n(uint32_t taddr, const float* v) {
+  if (N == 8) st8(taddr, v);
+  else st4(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void wait_ld_n(float* v) {
+  if (N == 8) wait_ld8(v);
+  else wait_ld4(v);
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // The softmax warps' and the epilogue warps' barriers, and votes over them.
-template <int ID>
-__device__ __forceinline__ void sync_four() { asm volatile("barrier.sync %0, 128;" ::"n"(ID) : "memory"); }
-template <int ID>
-__device__ __forceinline__ bool any_of_four(bool p) {
+template <int ID, int N>
+__device__ __forceinline__ void sync_of() { asm volatile("barrier.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
+template <int ID, int N>
+__device__ __forceinline__ bool any_of(bool p) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.red.or.pred b, %2, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r) : "r"((uint32_t)p), "n"(ID) : "memory");
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.red.or.pred b, %2, %3, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r) : "r"((uint32_t)p), "n"(ID), "n"(N) : "memory");
   return r;
 }
-__device__ __forceinline__ void softmax_sync() { sync_four<1>(); }
-__device__ __forceinline__ bool softmax_any(bool p) { return any_of_four<2>(p); }
-__device__ __forceinline__ void epilogue_sync() { sync_four<3>(); }
-__device__ __forceinline__ bool epilogue_any(bool p) { return any_of_four<4>(p); }
+__device__ __forceinline__ void softmax_sync() { sync_of<1, 256>(); }
+__device__ __forceinline__ bool softmax_any(bool p) { return any_of<2, 256>(p); }
+__device__ __forceinline__ void epilogue_sync() { sync_of<3, 128>(); }
+__device__ __forceinline__ bool epilogue_any(bool p) { return any_of<4, 128>(p); }
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -193,7 +225,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
   int ctas;
   if (!find_run<TM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) return;
 
-  if (warp == 8) {
+  if (warp == 12) {
     if (lane == 0) {
       for (int i = 0; i < S; ++i) {
         bar_init(&ctl->kv_full[i], 128 + 4);
@@ -203,11 +235,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         bar_init(&ctl->q_full[i], 64);
         bar_init(&ctl->q_empty[i], 1);
         bar_init(&ctl->s_full[i], 1);
-        bar_init(&ctl->p_full[i], 128);
+        bar_init(&ctl->p_full[i], 256);
         bar_init(&ctl->pv_done[i], 1);
         bar_init(&ctl->o_full[i], 1);
         bar_init(&ctl->o_empty[i], 128);
-        bar_init(&ctl->sum_full[i], 128);
+        bar_init(&ctl->sum_full[i], 256);
       }
       for (int i = 0; i < kItems; ++i) {
         bar_init(&ctl->item_full[i], 1);
@@ -234,18 +266,18 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     return ctl->item[it % kItems];
   };
 
-  // 128 registers at launch: the softmax warps, which hold scores and sums of all rows,
-  // take from the others (208 + 96 + 112 + 96 = 4 * 128)
-  if (warp >= 4 && warp < 12) {
-    if (warp < 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  // 96 registers at launch: the softmax warps, which hold scores and sums of their rows,
+  // take from the others (128 + 128 + 72 + 80 + 72 = 5 * 96)
+  if (warp >= 8 && warp < 16) {
+    if (warp < 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     }
-    if (warp < 8) {
+    if (warp < 12) {
       // -------------------------------------------------------------- loaders
       constexpr int LPR = C::kRow / 16, RPI = 32 / LPR;  // lanes per row, rows per pass
-      const int lw = warp - 4, jl = lane / LPR, cl = lane % LPR, key = lw * 32 + lane;
+      const int lw = warp - 8, jl = lane / LPR, cl = lane % LPR, key = lw * 32 + lane;
       const unsigned char* const base = reinterpret_cast<const unsigned char*>(P.pool) + cl * 16;
       const uint32_t vstep = (uint32_t)(P.H * P.pt);
       // places of this lane's chunks: the swizzle has NSW patterns
@@ -334,7 +366,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 9) {
+    } else if (warp == 13) {
       // ------------------------------------------------------ the run's items
       if (lane == 0) {
         for (uint32_t it = 0;; ++it) {
@@ -350,7 +382,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == 14) {
       // ----------------------------------------------------- q, positions
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
@@ -418,7 +450,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         if (last) break;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 8) {
+    } else if (warp == 12) {
       // ---------------------------------------------------------- MMA issuer
       {
         const uint32_t fmt = !F8 && DT == SLORA_BF16 ? 1u : 0u;
@@ -507,19 +539,25 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         wait(&ctl->fin, 0);
       }
     }
-  } else if (warp < 4) {
+  } else if (warp < 8) {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    constexpr int HM = TM / 8;
-    const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    // A thread owns a key and half of the rows, in units: of 4 rows where there are 8, else every
+    // other 8 rows.
+    constexpr int UN = TM == 8 ? 4 : 8, NU = TM == 8 ? 1 : TM / 16;
+    const int half = warp >> 2, wk = warp & 3, key = tid & 127;
+    auto row_of = [&](int u) { return TM == 8 ? half * 4 : (2 * u + half) * 8; };
+    auto s_col = [&](int r0) { return F8 ? r0 / 16 * 48 + r0 % 16 : r0; };
+    auto o_col = [&](int r0) { return F8 ? r0 / 16 * 48 + r0 % 16 : r0 / 8 * 16 + r0 % 8; };
+    constexpr int PS = F8 ? 16 : 8, NP = F8 ? 3 : 2;  // columns from piece to piece of O^T, pieces
+    const uint32_t ts = tmem + ((uint32_t)(wk * 32) << 16);
     const float* const scales = reinterpret_cast<const float*>(smem + C::kOffScale);
     uint32_t ti = 0, vslot = 1, vphase = 0;
-    float l[TM];  // this key's sums
+    float l[NU * UN];  // this key's sums
 #pragma unroll 1
     for (uint32_t it = 0;; ++it) {
       const Item& x_ = item_at(it);
       const int n_here = x_.n_tiles, tile0 = x_.tile, R = x_.R, flags = x_.flags;
-      const int NH = TM == 8 ? 1 : (R + 7) / 8;
       const uint32_t to = ts + 2 * C::kSCols + it % C::kOBufs * C::kPCols;
       wait(&ctl->rows_full[it % kItems], (it / kItems) & 1);
       const int* const pos = ctl->pos[it % kItems];
@@ -527,7 +565,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       const int pmin = pos[0], pmax = pos[R - 1];
       float vn = 0.f;
 #pragma unroll
-      for (int r = 0; r < TM; ++r) l[r] = 0.f;
+      for (int r = 0; r < NU * UN; ++r) l[r] = 0.f;
       if (tid < TM) ctl->ref[tid] = -INFINITY;
       softmax_sync();
 #pragma unroll 1
@@ -541,59 +579,64 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           vphase ^= 1;
         }
         tc_fence_after();
-        const uint32_t have = ctl->mask[ti % kMeta][warp];
+        const uint32_t have = ctl->mask[ti % kMeta][wk];
         float ks = 1.f, vs = 1.f;
         if (F8) {
-          ks = scales[(ti % kMeta) * 2 * kTK + tid];
-          vs = scales[((ti % kMeta) * 2 + 1) * kTK + tid];
+          ks = scales[(ti % kMeta) * 2 * kTK + key];
+          vs = scales[((ti % kMeta) * 2 + 1) * kTK + key];
         }
-        const int key0 = (tile0 + n) * kTK, j = key0 + tid;
+        const int key0 = (tile0 + n) * kTK, j = key0 + key;
         const bool open = have == FULL_MASK && key0 + kTK - 1 <= pmin && (A.window <= 0 || key0 > pmax - A.window);
         const bool mine = (have >> lane) & 1;
-        float s[TM];
+        float s[NU * UN];
         bool over = F8 && mine && vs > vn;
 #pragma unroll
-        for (int h = 0; h < HM; ++h) {
-          if (h < NH) {
-            float* const x = s + h * 8;
+        for (int u = 0; u < NU; ++u) {
+          const int r0 = row_of(u);
+          if (r0 < R) {
+            float* const x = s + u * UN;
+            const uint32_t col = sbuf + s_col(r0);
             if (!F8) {
-              ld8(sbuf + h * 8, x);
-              wait_ld8(x);
+              ld_n<UN>(col, x);
+              wait_ld_n<UN>(x);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] *= A.c;
+              for (int i = 0; i < UN; ++i) x[i] *= A.c;
             } else {
-              const uint32_t col = sbuf + h / 2 * 48 + (h & 1) * 8;
-              float y[8], z[8];
-              ld8(col, x);
-              ld8(col + 16, y);
-              ld8(col + 32, z);
-              wait_ld8(x);
-              wait_ld8(y);
-              wait_ld8(z);
+              float y[UN], z[UN];
+              ld_n<UN>(col, x);
+              ld_n<UN>(col + 16, y);
+              ld_n<UN>(col + 32, z);
+              wait_ld_n<UN>(x);
+              wait_ld_n<UN>(y);
+              wait_ld_n<UN>(z);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, x[i])) * (ks * qmul[h * 8 + i]);
+              for (int i = 0; i < UN; ++i) x[i] = fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, x[i])) * (ks * qmul[r0 + i]);
             }
             if (!open) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int p = pos[h * 8 + i];
+              for (int i = 0; i < UN; ++i) {
+                const int p = pos[r0 + i];
                 if (!mine || j > p || (A.window > 0 && j <= p - A.window)) x[i] = -INFINITY;
               }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) over |= x[i] > ctl->ref[h * 8 + i] + kSlack;
+            for (int i = 0; i < UN; ++i) over |= x[i] > ctl->ref[r0 + i] + kSlack;
           }
         }
         if (softmax_any(over)) {  // some reference moves: to the tile's maxima
 #pragma unroll
-          for (int r = 0; r < TM; ++r)
-            if (r < NH * 8) {
-              const float v = warp_max(s[r]);
-              if (lane == 0) ctl->red[warp][r] = v;
+          for (int u = 0; u < NU; ++u) {
+            if (row_of(u) < R) {
+#pragma unroll
+              for (int i = 0; i < UN; ++i) {
+                const float v = warp_max(s[u * UN + i]);
+                if (lane == 0) ctl->red[wk][row_of(u) + i] = v;
+              }
             }
-          if (F8) {
+          }
+          if (F8 && half == 0) {
             const float v = warp_max(mine ? vs : 0.f);
-            if (lane == 0) ctl->red[warp][TM] = v;
+            if (lane == 0) ctl->red[wk][TM] = v;
           }
           softmax_sync();
           float ratio = 1.f;
@@ -607,7 +650,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               vn = v;
             }
           }
-          if (tid < NH * 8) {
+          if (tid < (R + UN - 1) / UN * UN) {
             const int r = tid;
             const float top = fmaxf(fmaxf(ctl->red[0][r], ctl->red[1][r]), fmaxf(ctl->red[2][r], ctl->red[3][r]));
             const float m = ctl->ref[r], m1 = top > m + kSlack ? top : m;
@@ -620,68 +663,71 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           }
           softmax_sync();
 #pragma unroll
-          for (int h = 0; h < HM; ++h) {
-            if (h < NH) {
+          for (int u = 0; u < NU; ++u) {
+            const int r0 = row_of(u);
+            if (r0 < R) {
+              float f[UN];
+              bool same = true;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) l[h * 8 + i] *= ctl->fac[h * 8 + i];
-            }
-          }
-          if (n > 0) {
+              for (int i = 0; i < UN; ++i) {
+                const float a = ctl->fac[r0 + i];
+                l[u * UN + i] *= a;
+                f[i] = a * ratio;
+                same &= f[i] == 1.f;
+              }
+              if (n > 0 && !same) {
 #pragma unroll 1
-            for (int h = 0; h < NH; ++h) {
-#pragma unroll 1
-              for (int q = 0; q < (F8 ? 3 : 2); ++q) {
-                const uint32_t col = to + (F8 ? h / 2 * 48 + q * 16 + (h & 1) * 8 : h * 16 + q * 8);
-                float o[8];
-                ld8(col, o);
-                wait_ld8(o);
+                for (int q = 0; q < NP; ++q) {
+                  float o[UN];
+                  ld_n<UN>(to + o_col(r0) + q * PS, o);
+                  wait_ld_n<UN>(o);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] *= ctl->fac[h * 8 + i] * ratio;
-                st8(col, o);
+                  for (int i = 0; i < UN; ++i) o[i] *= f[i];
+                  st_n<UN>(to + o_col(r0) + q * PS, o);
+                }
               }
             }
           }
           wait_st();
         }
         // the weights of tile ti - 2 have been used: its products were issued before these scores
-        const uint32_t pd = sb + C::kOffP + (ti & 1) * C::kP + tid * 16;
+        const uint32_t pd = sb + C::kOffP + (ti & 1) * C::kP + key * 16;
         // relative V scale (a NaN scale of an unseen key stays out)
         const float f = F8 ? vs * __frcp_rn(fmaxf(vn, 0x1p-126f)) * kLift : kLift;
-        uint32_t q8[3][4];
 #pragma unroll
-        for (int h = 0; h < (HM + 1) / 2 * 2; ++h) {
-          if (h < NH || (F8 && (h & 1) && h < NH + 1)) {
-            uint32_t w[3][4] = {};
-            if (h < HM && h < NH) {
-              float p[8];
+        for (int u = 0; u < NU; ++u) {
+          const int r0 = row_of(u);
+          if (r0 < R) {
+            float p[UN];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = h < HM ? h * 8 + i : 0;
-                const float m = ctl->ref[r];
-                p[i] = ex2(s[r] - (m == -INFINITY ? 0.f : m));
-                l[r] += p[i];
-                if (F8) p[i] = s[r] == -INFINITY ? 0.f : p[i] * f;
-                else p[i] *= f;
-              }
-              if (!F8) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) split2<DT>(p[2 * i], p[2 * i + 1], w[0][i], w[1][i]);
+            for (int i = 0; i < UN; ++i) {
+              const float x = s[u * UN + i], m = ctl->ref[r0 + i];
+              p[i] = ex2(x - (m == -INFINITY ? 0.f : m));
+              l[u * UN + i] += p[i];
+              if (F8) {
+                p[i] = x == -INFINITY ? 0.f : p[i] * f;
+                p[i] = p[i] <= 448.f ? p[i] : NAN;  // never above, but an infinite scale
               } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = p[i] <= 448.f ? p[i] : NAN;  // never above, but an infinite scale
-#pragma unroll
-                for (int i = 0; i < 4; ++i) split3(p[2 * i], p[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+                p[i] *= f;
               }
             }
-            if (!F8) {
-              st_shared16(pd + (2 * h) * (kTK * 16), w[0][0], w[0][1], w[0][2], w[0][3]);
-              st_shared16(pd + (2 * h + 1) * (kTK * 16), w[1][0], w[1][1], w[1][2], w[1][3]);
-            } else {
+            uint32_t w[3][UN / 2];
 #pragma unroll
-              for (int q = 0; q < 3; ++q) {
-                q8[q][(h & 1) * 2] = w[q][0] | w[q][1] << 16;
-                q8[q][(h & 1) * 2 + 1] = w[q][2] | w[q][3] << 16;
-                if (h & 1) st_shared16(pd + (h / 2 * 3 + q) * (kTK * 16), q8[q][0], q8[q][1], q8[q][2], q8[q][3]);
+            for (int i = 0; i < UN / 2; ++i) {
+              if (!F8) split2<DT>(p[2 * i], p[2 * i + 1], w[0][i], w[1][i]);
+              else split3(p[2 * i], p[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+            }
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+              if (!F8) {
+                const uint32_t dst = pd + (r0 / 8 * 2 + q) * (kTK * 16) + r0 % 8 * 2;
+                if (UN == 8) st_shared16(dst, w[q][0], w[q][1], w[q][UN / 2 - 2], w[q][UN / 2 - 1]);
+                else st_shared8(dst, w[q][0], w[q][1]);
+              } else {
+                const uint32_t dst = pd + (r0 / 16 * 3 + q) * (kTK * 16) + r0 % 16;
+                const uint32_t a = w[q][0] | w[q][1] << 16;
+                if (UN == 8) st_shared8(dst, a, w[q][UN / 2 - 2] | w[q][UN / 2 - 1] << 16);
+                else st_shared4(dst, a);
               }
             }
           }
@@ -694,24 +740,25 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       // ---- the item's sums, for the epilogue (which is through with those of item it - 2)
       wait(&ctl->o_empty[it % C::kOBufs], ((it / C::kOBufs) & 1) ^ 1);
 #pragma unroll
-      for (int h = 0; h < HM; ++h) {
-        if (h < NH) {  // over the warp's keys: lane i * 4 ends with row i of the eight
-          float v[8];
+      for (int u = 0; u < NU; ++u) {
+        if (row_of(u) < R) {  // over the warp's keys: the lanes end in UN groups, one per row
+          float v[UN];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = l[h * 8 + i];
+          for (int i = 0; i < UN; ++i) v[i] = l[u * UN + i];
 #pragma unroll
-          for (int st = 0; st < 3; ++st) {
-            const int o = 16 >> st, half = 4 >> st;
-            const bool up = lane & o;
+          for (int o = 16, k = UN / 2; o >= 1; o >>= 1, k >>= 1) {
+            if (k >= 1) {
+              const bool up = lane & o;
 #pragma unroll
-            for (int i = 0; i < half; ++i) {
-              const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-              v[i] = keep + __shfl_xor_sync(FULL_MASK, give, o);
+              for (int i = 0; i < k; ++i) {
+                const float give = up ? v[i] : v[i + k], keep = up ? v[i + k] : v[i];
+                v[i] = keep + __shfl_xor_sync(FULL_MASK, give, o);
+              }
+            } else {
+              v[0] += __shfl_xor_sync(FULL_MASK, v[0], o);
             }
           }
-          v[0] += __shfl_xor_sync(FULL_MASK, v[0], 2);
-          v[0] += __shfl_xor_sync(FULL_MASK, v[0], 1);
-          if ((lane & 3) == 0) ctl->sum[it & 1][warp][h * 8 + (lane >> 2)] = v[0];
+          if (lane % (32 / UN) == 0) ctl->sum[it & 1][wk][row_of(u) + lane / (32 / UN)] = v[0];
         }
       }
       if (tid < TM) ctl->end_ref[it & 1][tid] = ctl->ref[tid];
@@ -721,8 +768,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     }
   } else {
     // ------------------------------------------- the rows of an item, or their partials
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    const int wl = warp - 12, tl = tid - 384;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const int wl = warp - 16, tl = tid - 512;
     const uint32_t ts = tmem + ((uint32_t)(wl * 32) << 16);
     const int d = D == 128 ? tl : wl * 16 + (lane & 15);
     const bool writes = D == 128 || lane < 16;
@@ -816,7 +863,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, C::kTmem);
+  if (warp == 12) tmem_dealloc(tmem, C::kTmem);
 }
 
 template <int DT, int FMT, int D, int TM>
@@ -828,42 +875,36 @@ cudaError_t run_decode(const KvAttnDev& A, int sm_count, RowClass cls, cudaStrea
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_decode<DT, FMT, D, TM>), bytes, sized);
   if (e != cudaSuccess) return e;
   k_kv_decode<DT, FMT, D, TM><<<sm_count, kNT, bytes, st>>>(A, cls);
-  const cudaError_t e2 = cudaGetLastError();
-  return e2 != cudaSuccess ? e2 : launch_combine<DT, D, TM>(A, sm_count, st);
+  return cudaGetLastError();
 }
 
-constexpr int max_rows_of(int fmt) { return fmt == SLORA_KV_16 ? 32 : 48; }
-
-// Row tiles as high as the call's largest sequence needs: the code for 8 rows is a fraction
-// of that for 48, and its ring is deeper.
 template <int DT, int FMT, int D>
-cudaError_t run_rows(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream_t st) {
-  const int64_t rows = (int64_t)A.G * A.max_rows;
-  if (rows <= 8) return run_decode<DT, FMT, D, 8>(A, sm_count, cls, st);
-  if (rows <= 16) return run_decode<DT, FMT, D, 16>(A, sm_count, cls, st);
-  return run_decode<DT, FMT, D, max_rows_of(FMT)>(A, sm_count, cls, st);
+cudaError_t run_rows(const KvAttnDev& A, int TM, int sm_count, RowClass cls, cudaStream_t st) {
+  if (TM == 8) return run_decode<DT, FMT, D, 8>(A, sm_count, cls, st);
+  if (TM == 16) return run_decode<DT, FMT, D, 16>(A, sm_count, cls, st);
+  return run_decode<DT, FMT, D, kv_stream_rows(FMT)>(A, sm_count, cls, st);
 }
 
 }  // namespace
 
 size_t kv_stream_workspace(int fmt, int D, int sm_count) {
-  return (size_t)sm_count * sizeof(Split) + 2 * (size_t)sm_count * slot_floats(max_rows_of(fmt), D) * 4;
+  return (size_t)sm_count * sizeof(Split) + 2 * (size_t)sm_count * slot_floats(kv_stream_rows(fmt), D) * 4;
 }
 
-cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s) {
-  const RowClass cls = {0, row_limit};
+cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int TM, int sm_count, cudaStream_t s) {
+  const RowClass cls = {0, kv_stream_rows(fmt)};
   if (D == 128) {
     if (dtype == SLORA_F16)
-      return fmt == SLORA_KV_16 ? run_rows<SLORA_F16, SLORA_KV_16, 128>(A, sm_count, cls, s)
-                                : run_rows<SLORA_F16, SLORA_KV_E4M3, 128>(A, sm_count, cls, s);
-    return fmt == SLORA_KV_16 ? run_rows<SLORA_BF16, SLORA_KV_16, 128>(A, sm_count, cls, s)
-                              : run_rows<SLORA_BF16, SLORA_KV_E4M3, 128>(A, sm_count, cls, s);
+      return fmt == SLORA_KV_16 ? run_rows<SLORA_F16, SLORA_KV_16, 128>(A, TM, sm_count, cls, s)
+                                : run_rows<SLORA_F16, SLORA_KV_E4M3, 128>(A, TM, sm_count, cls, s);
+    return fmt == SLORA_KV_16 ? run_rows<SLORA_BF16, SLORA_KV_16, 128>(A, TM, sm_count, cls, s)
+                              : run_rows<SLORA_BF16, SLORA_KV_E4M3, 128>(A, TM, sm_count, cls, s);
   }
   if (dtype == SLORA_F16)
-    return fmt == SLORA_KV_16 ? run_rows<SLORA_F16, SLORA_KV_16, 64>(A, sm_count, cls, s)
-                              : run_rows<SLORA_F16, SLORA_KV_E4M3, 64>(A, sm_count, cls, s);
-  return fmt == SLORA_KV_16 ? run_rows<SLORA_BF16, SLORA_KV_16, 64>(A, sm_count, cls, s)
-                            : run_rows<SLORA_BF16, SLORA_KV_E4M3, 64>(A, sm_count, cls, s);
+    return fmt == SLORA_KV_16 ? run_rows<SLORA_F16, SLORA_KV_16, 64>(A, TM, sm_count, cls, s)
+                              : run_rows<SLORA_F16, SLORA_KV_E4M3, 64>(A, TM, sm_count, cls, s);
+  return fmt == SLORA_KV_16 ? run_rows<SLORA_BF16, SLORA_KV_16, 64>(A, TM, sm_count, cls, s)
+                            : run_rows<SLORA_BF16, SLORA_KV_E4M3, 64>(A, TM, sm_count, cls, s);
 }
 
 }  // namespace slora

@@ -1278,16 +1278,15 @@ slora_status_t slora_kv_read(slora_pool* P, const slora_kv_layout_t* layout, voi
 
 // Whether a sequence of the call may have more rows per kv head than the stream
 // kernel takes.
-static bool kv_has_chunks(int G, int max_rows) { return (int64_t)G * max_rows > kKvStreamRows; }
+static bool kv_has_chunks(int fmt, int G, int max_rows) { return (int64_t)G * max_rows > kv_stream_rows(fmt); }
 
 size_t slora_kv_attention_workspace_bytes(const slora_pool* P, const slora_kv_layout_t* layout, int32_t n_q_heads,
                                           int32_t B, int32_t T, int32_t max_rows) {
   if (!P || !kv_layout_ok(layout) || n_q_heads < 1 || n_q_heads % layout->n_kv_heads || B < 1 || T < 1 || max_rows < 1)
     return 0;
   const size_t stream = kv_stream_workspace(layout->format, layout->head_dim, P->sm_count);
-  return kv_has_chunks(n_q_heads / layout->n_kv_heads, std::min(max_rows, T))
-             ? std::max(stream, kv_chunk_workspace(layout->head_dim, P->sm_count))
-             : stream;
+  const bool chunks = kv_has_chunks(layout->format, n_q_heads / layout->n_kv_heads, std::min(max_rows, T));
+  return chunks ? stream + kv_chunk_workspace(layout->head_dim, P->sm_count) : stream;
 }
 
 slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout, int32_t n_q_heads, const void* q,
@@ -1328,11 +1327,14 @@ slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout
   A.window = window;
   A.max_rows = std::min(max_rows, T);
   A.workspace = workspace;
+  A.chunk_workspace = static_cast<char*>(workspace) + kv_stream_workspace(layout->format, layout->head_dim, P->sm_count);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   phase(P, 0, 1, st);
-  CUDA_TRY(P, launch_kv_stream(A, P->d.dtype, layout->format, layout->head_dim, kKvStreamRows, P->sm_count, st));
-  if (kv_has_chunks(A.G, A.max_rows))
-    CUDA_TRY(P, launch_kv_chunk(A, P->d.dtype, layout->format, layout->head_dim, kKvStreamRows, P->sm_count, st));
+  const int fmt = layout->format, D = layout->head_dim, TM = kv_row_tile(fmt, (int64_t)A.G * A.max_rows);
+  const bool chunks = kv_has_chunks(fmt, A.G, A.max_rows);
+  CUDA_TRY(P, launch_kv_stream(A, P->d.dtype, fmt, D, TM, P->sm_count, st));
+  if (chunks) CUDA_TRY(P, launch_kv_chunk(A, P->d.dtype, fmt, D, P->sm_count, st));
+  CUDA_TRY(P, launch_kv_join(A, P->d.dtype, D, TM, chunks, P->sm_count, st));
   phase(P, 1, 1, st);
   return SLORA_OK;
 }

@@ -188,17 +188,26 @@ struct KvAttnDev {
   float c;                   // scale * log2(e)
   int window;                // 0: none
   int max_rows;
-  void* workspace;
+  void* workspace;           // of kv_decode.cu
+  void* chunk_workspace;     // of kv_chunk.cu
 };
 cudaError_t launch_kv_write(const KvDev& P, int dtype, int fmt, int D, const void* k, int64_t ldk, const void* v,
                             int64_t ldv, int sm_count, cudaStream_t s);
 cudaError_t launch_kv_read(const KvDev& P, int dtype, int fmt, int D, void* k, int64_t ldk, void* v, int64_t ldv,
                            int sm_count, cudaStream_t s);
-// Sequences of at most row_limit rows per kv head (kv_decode.cu), and of more (kv_chunk.cu).
-constexpr int kKvStreamRows = 64;
-cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s);
+// Attention: kv_decode.cu takes the sequences of up to kv_stream_rows rows per kv head, kv_chunk.cu
+// those of more, then the join of the items that were cut.  One row tile of kv_decode.cu is as far as
+// it goes: a second one would read the cache again, and kv_chunk.cu's cost of a key hardly depends on
+// the rows.  48 sequences over 1000..8000 keys, 8 kv heads of 128, 16-bit: 32 rows 134 us here and 162
+// there, 40 rows 218 and 164; e4m3: 48 rows 276 and 334.
+constexpr int kv_stream_rows(int fmt) { return fmt == SLORA_KV_16 ? 32 : 48; }
+// Rows of its row tiles, as many as the call's largest sequence needs: the code for 8 rows is a
+// fraction of that for 48, and its ring of copies is deeper.
+inline int kv_row_tile(int fmt, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kv_stream_rows(fmt); }
+cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int TM, int sm_count, cudaStream_t s);
 size_t kv_stream_workspace(int fmt, int D, int sm_count);
-cudaError_t launch_kv_chunk(const KvAttnDev& A, int dtype, int fmt, int D, int row_limit, int sm_count, cudaStream_t s);
+cudaError_t launch_kv_chunk(const KvAttnDev& A, int dtype, int fmt, int D, int sm_count, cudaStream_t s);
 size_t kv_chunk_workspace(int D, int sm_count);
+cudaError_t launch_kv_join(const KvAttnDev& A, int dtype, int D, int TM, bool chunks, int sm_count, cudaStream_t s);
 
 }  // namespace slora
