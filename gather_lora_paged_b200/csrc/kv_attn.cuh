@@ -58,12 +58,12 @@ struct Span {
 
 // Keys of rows [rt * TM, ...) of a sequence.
 template <int TM, int TK>
-__device__ __forceinline__ Span span_of(const KvSeq& s, int G, int window, int rt) {
-  const int R = s.n * G, r0 = rt * TM, r1 = min(R, r0 + TM) - 1;
+__device__ __forceinline__ Span span_of(const KvAttnDev& A, const KvSeq& s, int rt) {
+  const int R = s.n * A.G, r0 = rt * TM, r1 = min(R, r0 + TM) - 1;
   const int first = s.len - s.n;
   Span x;
-  x.hi = max(0, first + r1 / G + 1);
-  x.lo = window > 0 ? max(0, first + r0 / G - window + 1) : 0;
+  x.hi = max(0, first + token_of(A, r1) + 1);
+  x.lo = A.window > 0 ? max(0, first + token_of(A, r0) - A.window + 1) : 0;
   x.t0 = x.lo / TK;
   x.t1 = max(x.t0 + 1, (x.hi + TK - 1) / TK);
   return x;
@@ -81,7 +81,7 @@ __device__ __forceinline__ long long seq_tiles(const KvAttnDev& A, RowClass cls,
   const int RT = cdiv_i(s.n * A.G, TM);
   long long u = 0;
   for (int rt = 0; rt < RT; ++rt) {
-    const Span x = span_of<TM, TK>(s, A.G, A.window, rt);
+    const Span x = span_of<TM, TK>(A, s, rt);
     u += x.t1 - x.t0;
   }
   return u * A.kv.H;
@@ -101,13 +101,13 @@ struct Cursor {
     RT = cdiv_i(s.n * A.G, TM);
     long long per = 0;
     for (rt = 0; rt < RT; ++rt) {
-      x = span_of<TM, TK>(s, A.G, A.window, rt);
+      x = span_of<TM, TK>(A, s, rt);
       per += x.t1 - x.t0;
     }
-    h = (int)(off / per);
+    h = off < (1ll << 31) && per < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
     off -= h * per;
     for (rt = 0;; ++rt) {
-      x = span_of<TM, TK>(s, A.G, A.window, rt);
+      x = span_of<TM, TK>(A, s, rt);
       if (off < x.t1 - x.t0) break;
       off -= x.t1 - x.t0;
     }
@@ -130,11 +130,17 @@ struct Cursor {
         RT = cdiv_i(s.n * A.G, TM);
       }
     }
-    x = span_of<TM, TK>(s, A.G, A.window, rt);
+    x = span_of<TM, TK>(A, s, rt);
     tile = x.t0;
     return true;
   }
 };
+
+// a * b / c; the line is short enough for 32 bits nearly always.
+__device__ __forceinline__ long long share(long long a, int b, int c) {
+  if (a < (1 << 20) && b < (1 << 11)) return (uint32_t)a * (uint32_t)b / (uint32_t)c;
+  return a * b / c;
+}
 
 // This CTA's run of the line (all NT threads; sh: NT / 32 + 2 words of shared
 // memory, free again afterwards).  Runs are at least min_run tiles on average.
@@ -155,10 +161,10 @@ __device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int m
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) total += sh[i];
   __syncthreads();
-  ctas = (int)min((long long)gridDim.x, (total + min_run - 1) / min_run);
+  ctas = (int)min((long long)gridDim.x, total < (1ll << 31) ? (long long)(((uint32_t)total + min_run - 1) / min_run) : total);
   if ((int)blockIdx.x >= ctas) return false;
-  const long long u0 = total * blockIdx.x / ctas;
-  u1 = total * (blockIdx.x + 1) / ctas;
+  const long long u0 = share(total, blockIdx.x, ctas);
+  u1 = share(total, blockIdx.x + 1, ctas);
   long long base = 0;
   for (int b0 = 0;; b0 += NT) {  // the sequence that holds tile u0 (there is one: u0 < total)
     const int b = b0 + tid;
@@ -220,7 +226,8 @@ __device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK>
 // whose last tile is number end - 1 of the line.
 __device__ __forceinline__ void note_split(Split* sp, int b, int h, int rt, int slot, long long end, long long total,
                                            int ctas) {
-  const long long last = (end * ctas + total - 1) / total - 1;  // the run of tile end - 1
+  // the run of tile end - 1
+  const long long x = end * ctas + total - 1, last = (x < (1ll << 32) ? (uint32_t)x / (uint32_t)total : x / total) - 1;
   sp->b = b;
   sp->h = h;
   sp->rt = rt;

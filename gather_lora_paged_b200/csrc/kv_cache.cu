@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_write(KvDev P, const uint16_
                                                           int64_t ldv, int per_token) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per pass
   const int lane = threadIdx.x & 31, col = (lane % LPR) * 8;
-  if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX);
+  if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX, threadIdx.x, blockDim.x);
   const int units = P.T * per_token;
   for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
     const int t = u / per_token, r0 = (u - t * per_token) * (kIter * RPI) + lane / LPR;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_read(KvDev P, uint16_t* k, i
                                                          int per_token) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int lane = threadIdx.x & 31, col = (lane % LPR) * 8;
-  if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX);
+  if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX, threadIdx.x, blockDim.x);
   const int units = P.T * per_token;
   for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
     const int t = u / per_token, r0 = (u - t * per_token) * (kIter * RPI) + lane / LPR;

@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kNT = 512;
 constexpr int kTM = 256;      // rows per item
-constexpr int kTK = 128;      // keys per tile
+constexpr int kTK = kKvTile;  // keys per tile
 constexpr int kMinRun = 2;
 constexpr int kItems = 4;     // items that are known ahead
 constexpr int kMeta = 8;      // tiles whose scales and masks are kept

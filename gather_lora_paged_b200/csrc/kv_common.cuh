@@ -43,9 +43,9 @@ __device__ __forceinline__ bool kv_seq(const KvDev& P, int b, int max_rows, KvSe
          s.n <= max_rows;
 }
 
-// Records the sequences that kv_seq refuses (one CTA of a kernel does this).
-__device__ __forceinline__ void kv_record_bad(const KvDev& P, int max_rows) {
-  for (int b = threadIdx.x; b < P.B; b += blockDim.x) {
+// Records the sequences that kv_seq refuses (n threads of one CTA of a kernel do this).
+__device__ __forceinline__ void kv_record_bad(const KvDev& P, int max_rows, int thread, int n) {
+  for (int b = thread; b < P.B; b += n) {
     KvSeq s;
     if (!kv_seq(P, b, max_rows, s)) record_error(P.err, kErrKvSeq, b);
   }

@@ -27,7 +27,7 @@
 //   warps 16..19  an item's end: O^T from TMEM to the output, beside the next item.
 //
 // Weights are exp(s - m) with m a former maximum of the row: it moves (and O^T is
-// scaled) only when a score exceeds it by 2^3, which one vote per tile finds out.
+// scaled) only when a score exceeds it by 2^8 (16-bit) or 2^5 (e4m3), which one vote per tile finds out.
 //
 // What the tensor cores take is split so that nothing is lost that an output could show:
 // 16-bit: weights as hi + lo, two 16-bit columns of N.
@@ -35,8 +35,8 @@
 //         are sums of three e4m3 values, each 2^-4 of the one before and a
 //         column of its own: 12 bits, so an fp16 q is exact.  The largest of a q row lies in
 //         [2^7, 2^8) after a power of two, what is lost of any element is under 2^-26 of it;
-//         the weights reach 2^5 at m and 2^8 at most, what is lost is under 2^-23 of the
-//         row's largest.  K's row scale multiplies the score, V's the weight, relative to
+//         the weights are 2^3 at m and 2^8 at most, what is lost of each is under 2^-12 of
+//         it or 2^-21 of the row's largest.  K's row scale multiplies the score, V's the weight, relative to
 //         twice the largest V scale met so far.
 //
 // A key that a row does not see has weight 0, but 0 * inf is NaN: where a
@@ -51,17 +51,18 @@ namespace slora {
 namespace {
 
 constexpr int kNT = 640;       // threads
-constexpr int kTK = 128;       // keys per tile
+constexpr int kTK = kKvTile;   // keys per tile
 constexpr int kMinRun = 1;     // tiles that are worth a CTA of their own
 constexpr int kMeta = 8;       // tiles whose scales and masks are kept: what the ring holds, at least
 constexpr int kItems = 16;     // items that are known ahead
-constexpr float kSlack = 3.f;  // log2 by which scores may exceed the row's reference
-constexpr float kLift = 32.f;  // weight at the reference
 
 // TM: rows per item.  N is a multiple of 16 rows (e4m3: three columns a row).
 template <int FMT, int D, int TM>
 struct Cfg {
   static constexpr bool kF8 = FMT == SLORA_KV_E4M3;
+  // log2 by which scores may exceed the row's reference, and the weight at the reference: weights of
+  // up to 2^13 (fp16 ends at 2^16) and 2^8 (e4m3 ends at 2^8.8)
+  static constexpr float kSlack = kF8 ? 5.f : 8.f, kLift = kF8 ? 8.f : 32.f;
   static constexpr int kRow = KvRow<FMT, D>::kBytes;                    // a cached row
   static constexpr int kWidth = kRow >= 128 ? 128 : kRow;               // bytes of a row in a panel
   static constexpr int kPanel = kTK * kWidth;
@@ -88,7 +89,7 @@ struct Cfg {
 template <int TM, int S>
 struct Ctl {
   uint64_t kv_full[S], kv_empty[S], q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], rows_full[kItems];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], sum_full[2], fin;
+  uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], sum_full[2], tmem_full, fin;
   Item item[kItems];
   uint32_t tmem;
   int dead;                                   // a wait gave up: nobody waits any more
@@ -219,46 +220,47 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 
   griddep_launch();  // the join's CTAs may take their places (they wait for this grid's end)
   if (tid == 0) split->n = 0;
-  if (blockIdx.x == 0) kv_record_bad(P, A.max_rows);
+  if (warp == 12) {  // behind find_run's barriers when somebody needs them
+    for (int i = lane; i < S; i += 32) {
+      bar_init(&ctl->kv_full[i], 128 + 4);
+      bar_init(&ctl->kv_empty[i], 1);
+    }
+    if (lane < 2) {
+      bar_init(&ctl->q_full[lane], 64);
+      bar_init(&ctl->q_empty[lane], 1);
+      bar_init(&ctl->s_full[lane], 1);
+      bar_init(&ctl->p_full[lane], 256);
+      bar_init(&ctl->pv_done[lane], 1);
+      bar_init(&ctl->o_full[lane], 1);
+      bar_init(&ctl->o_empty[lane], 128);
+      bar_init(&ctl->sum_full[lane], 256);
+    }
+    if (lane < kItems) {
+      bar_init(&ctl->item_full[lane], 1);
+      bar_init(&ctl->item_empty[lane], 1);
+      bar_init(&ctl->rows_full[lane], 32);
+    }
+    if (lane == 0) {
+      bar_init(&ctl->tmem_full, 32);
+      bar_init(&ctl->fin, 1);
+      ctl->dead = 0;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   Cursor<TM, kTK> c;
   long long total, u1;
   int ctas;
-  if (!find_run<TM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) return;
-
-  if (warp == 12) {
-    if (lane == 0) {
-      for (int i = 0; i < S; ++i) {
-        bar_init(&ctl->kv_full[i], 128 + 4);
-        bar_init(&ctl->kv_empty[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        bar_init(&ctl->q_full[i], 64);
-        bar_init(&ctl->q_empty[i], 1);
-        bar_init(&ctl->s_full[i], 1);
-        bar_init(&ctl->p_full[i], 256);
-        bar_init(&ctl->pv_done[i], 1);
-        bar_init(&ctl->o_full[i], 1);
-        bar_init(&ctl->o_empty[i], 128);
-        bar_init(&ctl->sum_full[i], 256);
-      }
-      for (int i = 0; i < kItems; ++i) {
-        bar_init(&ctl->item_full[i], 1);
-        bar_init(&ctl->item_empty[i], 1);
-        bar_init(&ctl->rows_full[i], 32);
-      }
-      bar_init(&ctl->fin, 1);
-      ctl->dead = 0;
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncwarp();
-    tmem_alloc(&ctl->tmem, C::kTmem);
+  if (!find_run<TM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) {
+    if (blockIdx.x == 0) kv_record_bad(P, A.max_rows, tid, kNT);
+    return;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+
   const int n_tiles = (int)c.left;
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
+  auto tmem_at = [&]() -> uint32_t {  // for those who do not allocate it
+    wait(&ctl->tmem_full, 0);
+    return ctl->tmem;
+  };
   // An item's entry.  It is written again for item it + 16, once the epilogue is through with this
   // one; all others have read it by then.
   auto item_at = [&](uint32_t it) -> const Item& {
@@ -285,8 +287,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       uint32_t swz[NSW];
 #pragma unroll
       for (int k = 0; k < NSW; ++k) swz[k] = place<W>(kTK, k * RPI + jl, cl) - k * RPI * W;
-      uint32_t it = 0;
-      int left = 0, j = 0, lo = 0, hi = 0, b = 0, off = 0;  // the item whose tiles are looked up
+      // the item whose tiles are looked up: the first one is known here
+      uint32_t it = 1;
+      int left = (int)min((long long)(c.x.t1 - c.tile), c.left), j = c.tile * kTK + key, lo = c.x.lo, hi = c.x.hi, b = c.b,
+          off = c.h * P.pt;
       int pg[3], at[3], sq[3];  // page and place in it (-1: no such key) of this lane's key, three tiles
       auto fetch = [&](int i, int ti) {
         at[i] = -1;
@@ -336,10 +340,12 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             for (int k = 0; k < 32 / RPI; ++k)
               cp16(dst + k * RPI * W + swz[k % NSW], from + (uint64_t)rows[k] * C::kRow);
           } else {
-#pragma unroll
-            for (int k = 0; k < 32 / RPI; ++k) {
-              const bool real = (have >> (k * RPI + jl)) & 1;
-              cp16(dst + k * RPI * W + swz[k % NSW], real ? from + (uint64_t)rows[k] * C::kRow : base, real);
+#pragma unroll 1
+            for (int k = 0; k < 32 / RPI; ++k) {  // few tiles: little code rather than fast
+              const int x = k * RPI + jl;
+              const bool real = (have >> x) & 1;
+              const uint32_t r = __shfl_sync(FULL_MASK, row, x);
+              cp16(dst + place<W>(kTK, x, cl), real ? from + (uint64_t)r * C::kRow : base, real);
             }
           }
           if (part == 1) {
@@ -450,8 +456,14 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         if (last) break;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 15) {
+      if (blockIdx.x == 0) kv_record_bad(P, A.max_rows, lane, 32);
     } else if (warp == 12) {
       // ---------------------------------------------------------- MMA issuer
+      tmem_alloc(&ctl->tmem, C::kTmem);
+      __syncwarp();
+      const uint32_t tmem = ctl->tmem;
+      arrive(&ctl->tmem_full);
       {
         const uint32_t fmt = !F8 && DT == SLORA_BF16 ? 1u : 0u;
         // fp32 accumulators; K is K-major, V (bit 15) and the weights (bit 16) are MN-major
@@ -550,10 +562,15 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     auto s_col = [&](int r0) { return F8 ? r0 / 16 * 48 + r0 % 16 : r0; };
     auto o_col = [&](int r0) { return F8 ? r0 / 16 * 48 + r0 % 16 : r0 / 8 * 16 + r0 % 8; };
     constexpr int PS = F8 ? 16 : 8, NP = F8 ? 3 : 2;  // columns from piece to piece of O^T, pieces
-    const uint32_t ts = tmem + ((uint32_t)(wk * 32) << 16);
+    const uint32_t tmem = tmem_at(), ts = tmem + ((uint32_t)(wk * 32) << 16);
     const float* const scales = reinterpret_cast<const float*>(smem + C::kOffScale);
     uint32_t ti = 0, vslot = 1, vphase = 0;
     float l[NU * UN];  // this key's sums
+    // references and score multipliers: in registers where there are few
+    constexpr bool kRegs = NU == 1;
+    constexpr float kSlack = C::kSlack, kLift = C::kLift;
+    float mr[kRegs ? UN : 1] = {}, qm[kRegs ? UN : 1] = {};
+    auto refs = [&](int u, int i) { return kRegs ? mr[kRegs ? i : 0] : ctl->ref[row_of(u) + i]; };
 #pragma unroll 1
     for (uint32_t it = 0;; ++it) {
       const Item& x_ = item_at(it);
@@ -567,12 +584,20 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 #pragma unroll
       for (int r = 0; r < NU * UN; ++r) l[r] = 0.f;
       if (tid < TM) ctl->ref[tid] = -INFINITY;
+      if (kRegs) {
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+          mr[kRegs ? i : 0] = -INFINITY;
+          if (F8) qm[kRegs ? i : 0] = qmul[row_of(0) + i];
+        }
+      }
+      auto muls = [&](int u, int i) { return kRegs ? qm[kRegs ? i : 0] : qmul[row_of(u) + i]; };
       softmax_sync();
 #pragma unroll 1
       for (int n = 0; n < n_here; ++n, ++ti) {
         const uint32_t sbuf = ts + (ti & 1) * C::kSCols;
-        wait(&ctl->kv_full[vslot], vphase);  // scales and mask
-        wait(&ctl->s_full[ti & 1], (ti >> 1) & 1);
+        // scales and mask, scores
+        wait_for_both(&ctl->kv_full[vslot], vphase, &ctl->s_full[ti & 1], (ti >> 1) & 1, &ctl->dead, P.err);
         vslot += 2;
         if (vslot >= S) {
           vslot -= S;
@@ -610,7 +635,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               wait_ld_n<UN>(y);
               wait_ld_n<UN>(z);
 #pragma unroll
-              for (int i = 0; i < UN; ++i) x[i] = fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, x[i])) * (ks * qmul[r0 + i]);
+              for (int i = 0; i < UN; ++i) x[i] = fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, x[i])) * (ks * muls(u, i));
             }
             if (!open) {
 #pragma unroll
@@ -620,7 +645,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               }
             }
 #pragma unroll
-            for (int i = 0; i < UN; ++i) over |= x[i] > ctl->ref[r0 + i] + kSlack;
+            for (int i = 0; i < UN; ++i) over |= x[i] > refs(u, i) + kSlack;
           }
         }
         if (softmax_any(over)) {  // some reference moves: to the tile's maxima
@@ -674,6 +699,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
                 l[u * UN + i] *= a;
                 f[i] = a * ratio;
                 same &= f[i] == 1.f;
+                if (kRegs) mr[kRegs ? i : 0] = ctl->ref[r0 + i];
               }
               if (n > 0 && !same) {
 #pragma unroll 1
@@ -701,7 +727,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             float p[UN];
 #pragma unroll
             for (int i = 0; i < UN; ++i) {
-              const float x = s[u * UN + i], m = ctl->ref[r0 + i];
+              const float x = s[u * UN + i], m = refs(u, i);
               p[i] = ex2(x - (m == -INFINITY ? 0.f : m));
               l[u * UN + i] += p[i];
               if (F8) {
@@ -762,7 +788,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       if (tid < TM) ctl->end_ref[it & 1][tid] = ctl->ref[tid];
-      if (tid == 0) ctl->unit[it & 1] = (F8 ? vn : 1.f) * (1.f / kLift);
+      if (tid == 0) ctl->unit[it & 1] = (F8 ? vn : 1.f) * (1.f / C::kLift);
       arrive(&ctl->sum_full[it & 1]);
       if (flags & 4) break;
     }
@@ -770,7 +796,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     // ------------------------------------------- the rows of an item, or their partials
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int wl = warp - 16, tl = tid - 512;
-    const uint32_t ts = tmem + ((uint32_t)(wl * 32) << 16);
+    const uint32_t tmem = tmem_at(), ts = tmem + ((uint32_t)(wl * 32) << 16);
     const int d = D == 128 ? tl : wl * 16 + (lane & 15);
     const bool writes = D == 128 || lane < 16;
 #pragma unroll 1
@@ -863,7 +889,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, C::kTmem);
+  if (warp == 12) tmem_dealloc(ctl->tmem, C::kTmem);
 }
 
 template <int DT, int FMT, int D, int TM>

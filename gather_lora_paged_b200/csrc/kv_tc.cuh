@@ -96,5 +96,15 @@ __device__ __forceinline__ void wait_for(uint64_t* b, uint32_t parity, int* dead
   if (!done) wait_slow(b, parity, dead, err);
 }
 
+__device__ __forceinline__ void wait_for_both(uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc, int* dead, int32_t* err) {
+  uint32_t x, y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%2], %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%4], %5;\n\tselp.u32 %0, 1, 0, p;\n\tselp.u32 %1, 1, 0, q;\n\t}"
+      : "=r"(x), "=r"(y) : "r"(su32(b)), "r"(pb), "r"(su32(c)), "r"(pc) : "memory");
+  if (!x) wait_slow(b, pb, dead, err);
+  if (!y) wait_slow(c, pc, dead, err);
+}
+
 }  // namespace
 }  // namespace slora

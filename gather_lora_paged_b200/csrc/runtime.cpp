@@ -1334,7 +1334,8 @@ slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout
   const bool chunks = kv_has_chunks(fmt, A.G, A.max_rows);
   CUDA_TRY(P, launch_kv_stream(A, P->d.dtype, fmt, D, TM, P->sm_count, st));
   if (chunks) CUDA_TRY(P, launch_kv_chunk(A, P->d.dtype, fmt, D, P->sm_count, st));
-  CUDA_TRY(P, launch_kv_join(A, P->d.dtype, D, TM, chunks, P->sm_count, st));
+  // where every sequence fits one tile of keys no item is cut: nothing to join
+  if (A.kv.capacity > kKvTile) CUDA_TRY(P, launch_kv_join(A, P->d.dtype, D, TM, chunks, P->sm_count, st));
   phase(P, 1, 1, st);
   return SLORA_OK;
 }

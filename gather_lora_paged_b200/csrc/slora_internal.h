@@ -204,6 +204,7 @@ constexpr int kv_stream_rows(int fmt) { return fmt == SLORA_KV_16 ? 32 : 48; }
 // Rows of its row tiles, as many as the call's largest sequence needs: the code for 8 rows is a
 // fraction of that for 48, and its ring of copies is deeper.
 inline int kv_row_tile(int fmt, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kv_stream_rows(fmt); }
+constexpr int kKvTile = 128;  // keys
 cudaError_t launch_kv_stream(const KvAttnDev& A, int dtype, int fmt, int D, int TM, int sm_count, cudaStream_t s);
 size_t kv_stream_workspace(int fmt, int D, int sm_count);
 cudaError_t launch_kv_chunk(const KvAttnDev& A, int dtype, int fmt, int D, int sm_count, cudaStream_t s);
