@@ -47,66 +47,76 @@ __device__ __forceinline__ bool kv_locate(const KvDev& P, int t, int& b, int& po
   return pos >= 0;
 }
 
-// |value| of an e4m3 code.
-__device__ __forceinline__ float e4m3_abs(uint32_t code) {
-  const uint32_t h = e4m3x2_f16x2(code & 0x7f);
-  return __low2float(*reinterpret_cast<const __half2*>(&h));
+// Quantisation to the nearest code of the exact quotient q = x / scale, ties to even, with one product
+// per value.  With A = max|x| and borders m of two codes (at most 5 significant bits), x * 448 = m * A is an
+// equation of integers of at most 16 bits up to powers of two, so either it holds or x / A is off
+// m / 448 by 2^-16 (relative) at least.  Where it holds, q = m (A / 448) / scale is on the side of m on
+// which A / 448 is of its rounded value, for the whole row.  So x * rinv, rinv within 2^-22 of 1 / scale and
+// then moved by 2^-20 to that side, has q's code.  If 448 divides A without a rounding (or scale is the
+// least, a power of two), borders are met exactly: x * rinv is corrected by its residual (Markstein),
+// which makes it RN(q), the border itself there.
+struct RowScale {
+  float scale, rinv;
+  bool exact;
+};
+__device__ __forceinline__ float reciprocal(float x) {  // to one ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-
-// e4m3 code of the exact quotient x / scale, given rinv = RN(1 / scale).  The
-// product x * rinv is within 2^-22 of the quotient, so where its two neighbours
-// at that distance have one code, that is the code; where they do not, the
-// border m between their (adjacent) codes is compared with x exactly: m has 5
-// significant bits and scale 24, so m * scale is exact in 64 bits.
-__device__ __forceinline__ uint32_t e4m3_settle(float ax, float scale, uint32_t lo, uint32_t hi) {
-  const double m = 0.5 * ((double)e4m3_abs(lo) + (double)e4m3_abs(hi)) * (double)scale;
-  if ((double)ax > m) return hi;
-  if ((double)ax < m) return lo;
-  return (lo & 1) ? hi : lo;
+__device__ __forceinline__ RowScale row_scale(float most) {
+  // RN(most / 448): the product with RN(1 / 448) corrected by its residual, which is exact (all 16-bit
+  // values whose quotient is above 2^-126 have been tried)
+  const float c = 1.f / 448.f, q = most * c, s = fmaf(fmaf(-q, 448.f, most), c, q);
+  RowScale r;
+  r.scale = fmaxf(s, 0x1p-126f);
+  const float rest = fmaf(-s, 448.f, most);
+  r.exact = rest == 0.f || s < 0x1p-126f;
+  r.rinv = reciprocal(r.scale);
+  if (!r.exact) r.rinv *= rest > 0.f ? 1.f + 0x1p-20f : 1.f - 0x1p-20f;
+  return r;
 }
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {  // a in the low byte
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t quantise4(const float* f, float scale, float rinv) {
-  uint32_t lo = 0, hi = 0;
+__device__ __forceinline__ uint2 quantise8(const float* f, RowScale s) {
+  float q[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float a = f[2 * i] * rinv, b = f[2 * i + 1] * rinv;
-    lo |= cvt_e4m3x2(a * (1.0f - 0x1p-22f), b * (1.0f - 0x1p-22f)) << (16 * i);
-    hi |= cvt_e4m3x2(a * (1.0f + 0x1p-22f), b * (1.0f + 0x1p-22f)) << (16 * i);
-  }
-  if (lo != hi) {
+  for (int i = 0; i < 8; ++i) q[i] = f[i] * s.rinv;
+  if (s.exact) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t l = (lo >> (8 * i)) & 0xff, h = (hi >> (8 * i)) & 0xff;
-      if (l != h) {
-        const uint32_t c = e4m3_settle(fabsf(f[i]), scale, l & 0x7f, h & 0x7f) | (l & 0x80);
-        lo = (lo & ~(0xffu << (8 * i))) | (c << (8 * i));
-      }
-    }
+    for (int i = 0; i < 8; ++i) q[i] = fmaf(-fmaf(q[i], s.scale, -f[i]), s.rinv, q[i]);  // (signs that keep -0)
   }
-  return lo;
+  return make_uint2(cvt_e4m3x2(q[0], q[1]) | cvt_e4m3x2(q[2], q[3]) << 16, cvt_e4m3x2(q[4], q[5]) | cvt_e4m3x2(q[6], q[7]) << 16);
+}
+// The larger of two pairs of 15-bit magnitudes.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Units: (token, block of kIter * RPI of its 2 * H rows); a warp per unit.
 template <int DT, int FMT, int D>
 __global__ void __launch_bounds__(kWarps * 32) k_kv_write(KvDev P, const uint16_t* k, int64_t ldk, const uint16_t* v,
                                                           int64_t ldv, int per_token) {
+  constexpr int kRowBytes = KvRow<FMT, D>::kBytes;
   constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per pass
   const int lane = threadIdx.x & 31, col = (lane % LPR) * 8;
   if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX, threadIdx.x, blockDim.x);
   const int units = P.T * per_token;
   for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
     const int t = u / per_token, r0 = (u - t * per_token) * (kIter * RPI) + lane / LPR;
+    const uint16_t* const kt = k + (int64_t)t * ldk + col;
+    const uint16_t* const vt = v + (int64_t)t * ldv + col - P.H * D;
     uint4 x[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int r = r0 + i * RPI;
       if (r < 2 * P.H) {
-        const uint16_t* src = r < P.H ? k + (int64_t)t * ldk + (int64_t)r * D : v + (int64_t)t * ldv + (int64_t)(r - P.H) * D;
-        x[i] = __ldg(reinterpret_cast<const uint4*>(src + col));
+        x[i] = __ldg(reinterpret_cast<const uint4*>((r < P.H ? kt : vt) + r * D));
       } else {
         x[i] = make_uint4(0, 0, 0, 0);
       }
@@ -115,32 +125,37 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_write(KvDev P, const uint16_
     if (!kv_locate(P, t, b, pos)) continue;
     const uint32_t row = kv_row(P, b, pos, 0);
     if (row == kNoRow) continue;
+    unsigned char* const to = reinterpret_cast<unsigned char*>(P.pool) + (int64_t)row * kRowBytes + col * (kRowBytes / D);
+    float* const scales = FMT == SLORA_KV_E4M3 ? kv_scale(P, row) : nullptr;
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int r = r0 + i * RPI;
-      const uint32_t dst = row + (uint32_t)(r * P.pt);  // row r = (part, head)
+      const uint32_t off = (uint32_t)r * (uint32_t)P.pt;  // row r = (part, head): of the same page
       if (FMT == SLORA_KV_16) {
-        if (r < 2 * P.H) *reinterpret_cast<uint4*>(P.pool + (int64_t)dst * D + col) = x[i];
+        if (r < 2 * P.H) *reinterpret_cast<uint4*>(to + (int64_t)off * kRowBytes) = x[i];
       } else {
-        float f[8];
-        unpack8<DT>(x[i], f);
-        uint32_t top = 0;
+        // the largest magnitude, as a 16-bit pattern
+        uint32_t top = max_u16x2(max_u16x2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                 max_u16x2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+        for (int o = LPR / 2; o >= 1; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(FULL_MASK, top, o));
+        top = max(top & 0xffff, top >> 16);
         float scale = 0.f;
         uint2 codes = make_uint2(0, 0);
-        if (top >= 0x7f800000u) {
+        if (top >= (DT == SLORA_BF16 ? 0x7f80u : 0x7c00u)) {
           scale = __uint_as_float(0x7fc00000u);
         } else if (top) {
-          scale = fmaxf(__fdiv_rn(__uint_as_float(top), 448.f), 0x1p-126f);
-          const float rinv = __frcp_rn(scale);
-          codes = make_uint2(quantise4(f, scale, rinv), quantise4(f + 4, scale, rinv));
+          float f[8], most, zero;
+          unpack8<DT>(x[i], f);
+          if (DT == SLORA_BF16) most = __uint_as_float(top << 16);
+          else h2x2f(top, most, zero);
+          const RowScale rs = row_scale(most);
+          scale = rs.scale;
+          codes = quantise8(f, rs);
         }
         if (r < 2 * P.H) {
-          *reinterpret_cast<uint2*>(reinterpret_cast<unsigned char*>(P.pool) + (int64_t)dst * D + col) = codes;
-          if (col == 0) *kv_scale(P, dst) = scale;
+          *reinterpret_cast<uint2*>(to + (int64_t)off * kRowBytes) = codes;
+          if (col == 0) scales[off] = scale;
         }
       }
     }
