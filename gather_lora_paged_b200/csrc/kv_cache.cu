@@ -98,64 +98,73 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Units: (token, block of kIter * RPI of its 2 * H rows); a warp per unit.
+// A token's 2 * H rows come in blocks of kIter * RPI; a warp takes `blocks` of them in a row, the next
+// one's loads under way while it deals with one.
 template <int DT, int FMT, int D>
 __global__ void __launch_bounds__(kWarps * 32) k_kv_write(KvDev P, const uint16_t* k, int64_t ldk, const uint16_t* v,
-                                                          int64_t ldv, int per_token) {
+                                                          int64_t ldv, int blocks, int per_token) {
   constexpr int kRowBytes = KvRow<FMT, D>::kBytes;
   constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per pass
   const int lane = threadIdx.x & 31, col = (lane % LPR) * 8;
   if (blockIdx.x == 0) kv_record_bad(P, INT32_MAX, threadIdx.x, blockDim.x);
   const int units = P.T * per_token;
   for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
-    const int t = u / per_token, r0 = (u - t * per_token) * (kIter * RPI) + lane / LPR;
+    const int t = u / per_token, first = (u - t * per_token) * blocks * (kIter * RPI);
+    const int end = min(2 * P.H, first + blocks * (kIter * RPI));
     const uint16_t* const kt = k + (int64_t)t * ldk + col;
     const uint16_t* const vt = v + (int64_t)t * ldv + col - P.H * D;
-    uint4 x[kIter];
+    uint4 next[kIter];
+    auto load = [&](int r0) {
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const int r = r0 + i * RPI;
-      if (r < 2 * P.H) {
-        x[i] = __ldg(reinterpret_cast<const uint4*>((r < P.H ? kt : vt) + r * D));
-      } else {
-        x[i] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kIter; ++i) {
+        const int r = r0 + i * RPI;
+        next[i] = make_uint4(0, 0, 0, 0);
+        if (r < end) next[i] = __ldg(reinterpret_cast<const uint4*>((r < P.H ? kt : vt) + r * D));
       }
-    }
+    };
+    load(first + lane / LPR);
     int b, pos;
     if (!kv_locate(P, t, b, pos)) continue;
     const uint32_t row = kv_row(P, b, pos, 0);
     if (row == kNoRow) continue;
     unsigned char* const to = reinterpret_cast<unsigned char*>(P.pool) + (int64_t)row * kRowBytes + col * (kRowBytes / D);
     float* const scales = FMT == SLORA_KV_E4M3 ? kv_scale(P, row) : nullptr;
+#pragma unroll 1
+    for (int r0 = first + lane / LPR; r0 - lane / LPR < end; r0 += kIter * RPI) {
+      uint4 x[kIter];
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const int r = r0 + i * RPI;
-      const uint32_t off = (uint32_t)r * (uint32_t)P.pt;  // row r = (part, head): of the same page
-      if (FMT == SLORA_KV_16) {
-        if (r < 2 * P.H) *reinterpret_cast<uint4*>(to + (int64_t)off * kRowBytes) = x[i];
-      } else {
-        // the largest magnitude, as a 16-bit pattern
-        uint32_t top = max_u16x2(max_u16x2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                 max_u16x2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+      for (int i = 0; i < kIter; ++i) x[i] = next[i];
+      if (r0 - lane / LPR + kIter * RPI < end) load(r0 + kIter * RPI);
 #pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(FULL_MASK, top, o));
-        top = max(top & 0xffff, top >> 16);
-        float scale = 0.f;
-        uint2 codes = make_uint2(0, 0);
-        if (top >= (DT == SLORA_BF16 ? 0x7f80u : 0x7c00u)) {
-          scale = __uint_as_float(0x7fc00000u);
-        } else if (top) {
-          float f[8], most, zero;
-          unpack8<DT>(x[i], f);
-          if (DT == SLORA_BF16) most = __uint_as_float(top << 16);
-          else h2x2f(top, most, zero);
-          const RowScale rs = row_scale(most);
-          scale = rs.scale;
-          codes = quantise8(f, rs);
-        }
-        if (r < 2 * P.H) {
-          *reinterpret_cast<uint2*>(to + (int64_t)off * kRowBytes) = codes;
-          if (col == 0) scales[off] = scale;
+      for (int i = 0; i < kIter; ++i) {
+        const int r = r0 + i * RPI;
+        const uint32_t off = (uint32_t)r * (uint32_t)P.pt;  // row r = (part, head): of the same page
+        if (FMT == SLORA_KV_16) {
+          if (r < end) *reinterpret_cast<uint4*>(to + (int64_t)off * kRowBytes) = x[i];
+        } else {
+          // the largest magnitude, as a 16-bit pattern
+          uint32_t top = max_u16x2(max_u16x2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                   max_u16x2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+#pragma unroll
+          for (int o = LPR / 2; o >= 1; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(FULL_MASK, top, o));
+          top = max(top & 0xffff, top >> 16);
+          float scale = 0.f;
+          uint2 codes = make_uint2(0, 0);
+          if (top >= (DT == SLORA_BF16 ? 0x7f80u : 0x7c00u)) {
+            scale = __uint_as_float(0x7fc00000u);
+          } else if (top) {
+            float f[8], most, zero;
+            unpack8<DT>(x[i], f);
+            if (DT == SLORA_BF16) most = __uint_as_float(top << 16);
+            else h2x2f(top, most, zero);
+            const RowScale rs = row_scale(most);
+            scale = rs.scale;
+            codes = quantise8(f, rs);
+          }
+          if (r < end) {
+            *reinterpret_cast<uint2*>(to + (int64_t)off * kRowBytes) = codes;
+            if (col == 0) scales[off] = scale;
+          }
         }
       }
     }
@@ -232,10 +241,15 @@ Grid grid_for(const KvDev& P, int D, int sm_count) {
 
 cudaError_t launch_kv_write(const KvDev& P, int dtype, int fmt, int D, const void* k, int64_t ldk, const void* v,
                             int64_t ldv, int sm_count, cudaStream_t s) {
-  const Grid g = grid_for(P, D, sm_count);
+  // a token's rows are spread over warps while there are fewer of these than the GPU holds
+  const int all = cdiv_i(2 * P.H, kIter * 32 / (D / 8));
+  const int64_t each = (int64_t)P.T * all / ((int64_t)sm_count * 40);
+  const int blocks = (int)(each < 1 ? 1 : each > all ? all : each), per_token = cdiv_i(all, blocks);
+  const int64_t ctas = ((int64_t)P.T * per_token + kWarps - 1) / kWarps;
+  const int grid = (int)(ctas < (int64_t)sm_count * 8 ? ctas : (int64_t)sm_count * 8);
   auto go = [&](auto kern) {
-    kern<<<g.grid, kWarps * 32, 0, s>>>(P, static_cast<const uint16_t*>(k), ldk, static_cast<const uint16_t*>(v), ldv,
-                                        g.per_token);
+    kern<<<grid, kWarps * 32, 0, s>>>(P, static_cast<const uint16_t*>(k), ldk, static_cast<const uint16_t*>(v), ldv, blocks,
+                                      per_token);
     return cudaGetLastError();
   };
   if (fmt == SLORA_KV_16)  // a copy: the element type does not matter
