@@ -124,21 +124,16 @@ def lib():
 # marshalling helpers
 def _ptr(t) -> int | None:
     """Device/host pointer of a tensor, an int, or None."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
-    return t.ctypes.data  # numpy array (host memory)
+    except AttributeError:
+        return t.ctypes.data  # numpy array (host memory)
 
 
 def _stream(s) -> int | None:
-    if s is None:
-        return None
-    if isinstance(s, int):
-        return s
-    return s.cuda_stream
+    return s if s is None or isinstance(s, int) else s.cuda_stream
 
 
 def _event(e) -> int | None:
@@ -297,14 +292,18 @@ def slora_kv_check_batch(pool: int, layout: KvLayout, row_start, kv_len, blocks,
 
 def slora_kv_write(pool: int, layout: KvLayout, k, ldk: int, v, ldv: int, row_start, kv_len, blocks, ldb: int,
                    B: int, T: int, stream=None) -> None:
-    _check(pool, lib().slora_kv_write(pool, layout, _ptr(k), ldk, _ptr(v), ldv, _ptr(row_start), _ptr(kv_len),
-                                      _ptr(blocks), ldb, B, T, _stream(stream)))
+    status = lib().slora_kv_write(pool, layout, _ptr(k), ldk, _ptr(v), ldv, _ptr(row_start), _ptr(kv_len),
+                                  _ptr(blocks), ldb, B, T, _stream(stream))
+    if status:
+        _check(pool, status)
 
 
 def slora_kv_read(pool: int, layout: KvLayout, k, ldk: int, v, ldv: int, row_start, kv_len, blocks, ldb: int,
                   B: int, T: int, stream=None) -> None:
-    _check(pool, lib().slora_kv_read(pool, layout, _ptr(k), ldk, _ptr(v), ldv, _ptr(row_start), _ptr(kv_len),
-                                     _ptr(blocks), ldb, B, T, _stream(stream)))
+    status = lib().slora_kv_read(pool, layout, _ptr(k), ldk, _ptr(v), ldv, _ptr(row_start), _ptr(kv_len),
+                                 _ptr(blocks), ldb, B, T, _stream(stream))
+    if status:
+        _check(pool, status)
 
 
 def slora_kv_attention(pool: int, layout: KvLayout, n_q_heads: int, q, ldq: int, out, ldo: int, lse, row_start,
@@ -312,10 +311,12 @@ def slora_kv_attention(pool: int, layout: KvLayout, n_q_heads: int, q, ldq: int,
                        workspace, stream=None) -> None:
     """lse: a float32 tensor or None; workspace: a device tensor of at least
     slora_kv_attention_workspace_bytes() bytes."""
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(pool, lib().slora_kv_attention(pool, layout, n_q_heads, _ptr(q), ldq, _ptr(out), ldo, _ptr(lse),
-                                          _ptr(row_start), _ptr(kv_len), _ptr(blocks), ldb, B, T, max_rows, scale,
-                                          window, _ptr(workspace), size, _stream(stream)))
+    size = 0 if workspace is None else workspace.nbytes
+    status = lib().slora_kv_attention(pool, layout, n_q_heads, _ptr(q), ldq, _ptr(out), ldo, _ptr(lse), _ptr(row_start),
+                                      _ptr(kv_len), _ptr(blocks), ldb, B, T, max_rows, scale, window, _ptr(workspace),
+                                      size, _stream(stream))
+    if status:
+        _check(pool, status)
 
 
 def slora_kv_attention_workspace_bytes(pool: int, layout: KvLayout, n_q_heads: int, B: int, T: int,
