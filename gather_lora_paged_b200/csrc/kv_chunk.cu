@@ -26,6 +26,8 @@
 // that is raised when a tile's largest is 8 times it.
 #include <math.h>
 
+#include <type_traits>
+
 #include "kv_attn.cuh"
 #include "kv_tc.cuh"
 
@@ -56,7 +58,7 @@ struct Cfg {
 template <int S>
 struct Ctl {
   uint64_t kv_full[S], kv_empty[S], q_full, q_empty, item_full[kItems], item_empty[kItems], rows_full[kItems];
-  uint64_t s_full[2], p_full[2], o_full[2], fin;
+  uint64_t s_full[2], p_full[2][2], o_full[2], fin;  // p_full[q tile][half of the keys]
   Item item[kItems];
   uint32_t tmem;
   int dead;                    // a wait gave up: nobody waits any more
@@ -74,6 +76,11 @@ __device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -110,6 +117,11 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* u) {
       "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
       "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // tcgen05.wait::ld, tied to the registers that a load fills
 __device__ __forceinline__ void wait_ld32(float* v) {
@@ -178,7 +190,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       }
       for (int i = 0; i < 2; ++i) {
         bar_init(&ctl->s_full[i], 1);
-        bar_init(&ctl->p_full[i], 128);
+        bar_init(&ctl->p_full[i][0], 128);
+        bar_init(&ctl->p_full[i][1], 128);
         bar_init(&ctl->o_full[i], 1);
       }
       bar_init(&ctl->fin, 1);
@@ -238,11 +251,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         }
         mma_commit(&ctl->s_full[i]);
       };
-      auto pv = [&](int i, uint32_t slot, bool first) {
-        const uint32_t b = v_lo + slot * (C::kSlot >> 4);
+      auto pv = [&](int i, int half, uint32_t slot, bool first) {
+        const uint32_t b = v_lo + slot * (C::kSlot >> 4) + half * ((kTK / 32 * 2048) >> 4), a = tmem + i * 128 + half * 32;
 #pragma unroll
-        for (int k = 0; k < kTK / 16; ++k)
-          mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b + ((k * 2048) >> 4), hi, id_o, !(first && k == 0));
+        for (int k = 0; k < kTK / 32; ++k)
+          mma_ts(tmem + 256 + i * 128, a + k * 8, b + ((k * 2048) >> 4), hi, id_o, !(first && half == 0 && k == 0));
       };
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
@@ -265,11 +278,15 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           const bool more = n + 1 < n_tiles;
           const uint32_t v = (g + 1) % S, k = (g + 2) % S;
           wait(&ctl->kv_full[v], ((g + 1) / S) & 1);
-          wait(&ctl->p_full[0], pn++ & 1);
+          wait(&ctl->p_full[0][0], pn & 1);
           fence_async_smem();
           tc_fence_after();
+          if (elect_one()) pv(0, 0, v, n == 0);
+          __syncwarp();
+          wait(&ctl->p_full[0][1], pn++ & 1);
+          tc_fence_after();
           if (elect_one()) {
-            pv(0, v, n == 0);
+            pv(0, 1, v, n == 0);
             if (!more) mma_commit(&ctl->o_full[0]);
           }
           __syncwarp();
@@ -281,12 +298,16 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
             __syncwarp();
           }
           if (two) {
-            wait(&ctl->p_full[1], pn1++ & 1);
+            wait(&ctl->p_full[1][0], pn1 & 1);
+            tc_fence_after();
+            if (elect_one()) pv(1, 0, v, n == 0);
+            __syncwarp();
+            wait(&ctl->p_full[1][1], pn1++ & 1);
             tc_fence_after();
           }
           if (elect_one()) {
             if (two) {
-              pv(1, v, n == 0);
+              pv(1, 1, v, n == 0);
               if (!more) mma_commit(&ctl->o_full[1]);
             }
             mma_commit(&ctl->kv_empty[v]);
@@ -491,50 +512,56 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
 #pragma unroll 1
         for (int n = 0; n < n_tiles; ++n, ++ti) {
           const uint32_t g = 2 * ti + 1;
-          wait(&ctl->kv_full[g % S], (g / S) & 1);  // scales and mask
-          wait(&ctl->s_full[wg], sn++ & 1);
+          // scales and mask, scores
+          wait_for_both(&ctl->kv_full[g % S], (g / S) & 1, &ctl->s_full[wg], sn++ & 1, &ctl->dead, P.err);
           tc_fence_after();
           float s[kTK];
-#pragma unroll
-          for (int i = 0; i < kTK; i += 32) ld32(ts + i, s + i);
-#pragma unroll
-          for (int i = 0; i < kTK; i += 32) wait_ld32(s + i);
+          ld32(ts, s);
+          ld32(ts + 32, s + 32);
           const float* const ks = scales + (ti % kMeta) * 2 * kTK;
-          if (F8) {
-#pragma unroll
-            for (int i = 0; i < kTK; i += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(ks + i);
-              s[i] *= k4.x;
-              s[i + 1] *= k4.y;
-              s[i + 2] *= k4.z;
-              s[i + 3] *= k4.w;
-            }
-          }
           const int key0 = (tile0 + n) * kTK;
           const uint4 have = *reinterpret_cast<const uint4*>(ctl->mask[ti % kMeta]);
           const bool masked = key0 + kTK - 1 > pmin || (A.window > 0 && key0 <= pmax - A.window) ||
                               (have.x & have.y & have.z & have.w) != FULL_MASK;
-          if (masked) {
-            const int hi = pos - key0, lo = low - key0;
-            const uint32_t hv[4] = {have.x, have.y, have.z, have.w};
+          const uint32_t hv[4] = {have.x, have.y, have.z, have.w};
+          float top[2] = {-INFINITY, -INFINITY};
+          // scales, masks and maxima of 32 scores
+          auto take = [&](int w) {
+            float* const x = s + w * 32;
+            if (F8) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              // bits of the keys lo < i <= hi
-              const int h2 = min(max(hi - 32 * w + 1, 0), 32), l2 = min(max(lo - 32 * w + 1, 0), 32);
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(ks + w * 32 + i);
+                unpair(mul2(pair(x[i], x[i + 1]), k4.x), x[i], x[i + 1]);
+                unpair(mul2(pair(x[i + 2], x[i + 3]), k4.y), x[i + 2], x[i + 3]);
+              }
+            }
+            if (masked) {  // bits of the keys lo < i <= hi
+              const int hi = pos - key0 - 32 * w + 1, lo = low - key0 - 32 * w + 1;
+              const int h2 = min(max(hi, 0), 32), l2 = min(max(lo, 0), 32);
               const uint32_t below_h = h2 == 32 ? FULL_MASK : (1u << h2) - 1, below_l = l2 == 32 ? FULL_MASK : (1u << l2) - 1;
               const uint32_t seen = hv[w] & below_h & ~below_l;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (!((seen >> i) & 1)) s[w * 32 + i] = -INFINITY;
+                if (!((seen >> i) & 1)) x[i] = -INFINITY;
             }
-          }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kTK; i += 8) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) top[q] = fmaxf(fmaxf(top[q], s[i + 2 * q]), s[i + 2 * q + 1]);
-          }
-          const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cr);
+            for (int i = 0; i < 32; i += 4) {
+              top[0] = max3(top[0], x[i], x[i + 1]);
+              top[1] = max3(top[1], x[i + 2], x[i + 3]);
+            }
+          };
+          wait_ld32(s);
+          wait_ld32(s + 32);
+          take(0);
+          take(1);
+          ld32(ts + 64, s + 64);
+          ld32(ts + 96, s + 96);
+          wait_ld32(s + 64);
+          wait_ld32(s + 96);
+          take(2);
+          take(3);
+          const float mn = fmaxf(m, fmaxf(top[0], top[1]) * cr);
           float ratio = 1.f;
           bool raise = false;
           if (F8) {
@@ -566,40 +593,49 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           }
           const float mz = m == -INFINITY ? 0.f : m;
           const float vinv = F8 ? __frcp_rn(vn) : 1.f;
-          const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz);
-          uint64_t ls[4] = {0, 0, 0, 0};
+          const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz), vi2 = pair(vinv, vinv);
+          uint64_t ls[2] = {0, 0};
+          auto weigh = [&](auto all_seen) {  // the weights, from the scores
+            constexpr bool kOpen = decltype(all_seen)::value;
 #pragma unroll
-          for (int i = 0; i < kTK; i += 32) {
-            uint32_t w[16];
+            for (int i = 0; i < kTK; i += 32) {
+              uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              float p[4];
-#pragma unroll
-              for (int q = 0; q < 4; q += 2) {
-                unpair(fma2(pair(s[i + k + q], s[i + k + q + 1]), c2, m2), p[q], p[q + 1]);
-                p[q] = ex2(p[q]);
-                p[q + 1] = ex2(p[q + 1]);
-                ls[(k >> 1 & 2) + (q >> 1)] = add2(ls[(k >> 1 & 2) + (q >> 1)], pair(p[q], p[q + 1]));
+              for (int k = 0; k < 32; k += 2) {
+                float p[2];
+                unpair(fma2(pair(s[i + k], s[i + k + 1]), c2, m2), p[0], p[1]);
+                p[0] = ex2(p[0]);
+                p[1] = ex2(p[1]);
+                uint64_t pp = pair(p[0], p[1]);
+                ls[(k >> 1) & 1] = add2(ls[(k >> 1) & 1], pp);
+                if (F8) {
+                  pp = mul2(pp, mul2(*reinterpret_cast<const uint64_t*>(ks + kTK + i + k), vi2));
+                  float q[2];
+                  unpair(pp, q[0], q[1]);
+                  if (!kOpen) {  // a NaN scale of an unseen key stays out
+                    q[0] = p[0] == 0.f ? 0.f : q[0];
+                    q[1] = p[1] == 0.f ? 0.f : q[1];
+                  }
+                  w[k / 2] = pk2<MT>(q[0], q[1]);
+                } else {
+                  w[k / 2] = pk2<MT>(p[0], p[1]);
+                }
               }
-              if (F8) {
-                const float4 v4 = *reinterpret_cast<const float4*>(ks + kTK + i + k);
-                const float f[4] = {v4.x * vinv, v4.y * vinv, v4.z * vinv, v4.w * vinv};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) p[q] = masked && p[q] == 0.f ? 0.f : p[q] * f[q];  // a NaN scale of an unseen key stays out
+              st16(ts + i / 2, w);
+              if (i == 32 || i == 96) {  // the products with half of the keys may begin
+                wait_st();
+                tc_fence_before();
+                arrive(&ctl->p_full[wg][i / 64]);
               }
-              w[k / 2] = pk2<MT>(p[0], p[1]);
-              w[k / 2 + 1] = pk2<MT>(p[2], p[3]);
             }
-            st16(ts + i / 2, w);
-          }
+          };
+          if (masked) weigh(std::false_type{});
+          else weigh(std::true_type{});
           {
             float a, b;
-            unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), a, b);
+            unpair(add2(ls[0], ls[1]), a, b);
             l += a + b;
           }
-          wait_st();
-          tc_fence_before();
-          arrive(&ctl->p_full[wg]);
         }
 
         // ---- the rows of this item, or their partials
