@@ -33,11 +33,12 @@
 // 16-bit: weights as hi + lo, two 16-bit columns of N.
 // e4m3:   the codes are operands as they are (kind::f8f6f4), and q and the weights
 //         are sums of three e4m3 values, each 2^-4 of the one before and a
-//         column of its own: 12 bits, so an fp16 q is exact.  The largest of a q row lies in
-//         [2^7, 2^8) after a power of two, what is lost of any element is under 2^-26 of it;
-//         the weights are 2^3 at m and 2^8 at most, what is lost of each is under 2^-12 of
-//         it or 2^-21 of the row's largest.  K's row scale multiplies the score, V's the weight, relative to
-//         twice the largest V scale met so far.
+//         column of its own: 12 bits, so an fp16 q is exact, and a weight is its fp16 value.  The
+//         largest of a q row lies in [2^7, 2^8) after a power of two, what is lost of any element is under
+//         2^-26 of it; the weights are 2^3 at m and 2^8 at most, what is lost of each is under 2^-11 of
+//         it or 2^-21 of the row's largest (as fp32 pieces 2^-12, for a tenth of the time of a tile).
+//         K's row scale multiplies the score, V's the weight, relative to twice the largest V scale
+//         met so far.
 //
 // A key that a row does not see has weight 0, but 0 * inf is NaN: where a
 // masked V row holds an infinity or a NaN, the rows that it spoiled are seen to be not
@@ -55,6 +56,7 @@ constexpr int kTK = kKvTile;   // keys per tile
 constexpr int kMinRun = 1;     // tiles that are worth a CTA of their own
 constexpr int kMeta = 8;       // tiles whose scales and masks are kept: what the ring holds, at least
 constexpr int kItems = 16;     // items that are known ahead
+constexpr float kNoRef = 0x1.fffffep127f;  // (negated) reference of a row that has seen no key
 
 // TM: rows per item.  N is a multiple of 16 rows (e4m3: three columns a row).
 template <int FMT, int D, int TM>
@@ -94,10 +96,10 @@ struct Ctl {
   uint32_t tmem;
   int dead;                                   // a wait gave up: nobody waits any more
   uint32_t mask[kMeta][4];                    // keys of a tile that are there
-  float qmul[kItems][(TM + 15) / 16 * 16];    // score multipliers of an item's rows
+  alignas(16) float qmul[kItems][(TM + 15) / 16 * 16];    // score multipliers of an item's rows
   int pos[kItems][(TM + 15) / 16 * 16];       // their positions (-1: no such row)
   float red[4][TM + 4];                       // warps' maxima
-  float ref[TM];                              // the rows' references
+  alignas(16) float ref[TM];                  // the rows' references, negated
   float fac[TM];                              // what a move of them scales sums by
   // an item's end, for the epilogue: warps' sums, references, the weights' unit, and its own notes
   float sum[2][4][TM], end_ref[2][TM], unit[2], out_fac[TM];
@@ -174,15 +176,25 @@ __device__ __forceinline__ void softmax_sync() { sync_of<1, 256>(); }
 __device__ __forceinline__ bool softmax_any(bool p) { return any_of<2, 256>(p); }
 __device__ __forceinline__ void epilogue_sync() { sync_of<3, 128>(); }
 __device__ __forceinline__ bool epilogue_any(bool p) { return any_of<4, 128>(p); }
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
+}
+// Two weights as three e4m3 codes each, every one 2^-4 of the one before: of their fp16 values, whose 11 bits
+// they hold.
+__device__ __forceinline__ void split3_weights(uint64_t w, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  float a, b;
+  unpair(w, a, b);
+  asm("{\n\t.reg .b32 h, c, s;\n\t.reg .b16 k;\n\t"
+      "mov.b32 s, 0x4c004c00;\n\t"                      // 16, 16
+      "cvt.rn.f16x2.f32 h, %4, %3;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %0, k;\n\tcvt.rn.f16x2.e4m3x2 c, k;\n\t"
+      "sub.f16x2 h, h, c;\n\tmul.f16x2 h, h, s;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %1, k;\n\tcvt.rn.f16x2.e4m3x2 c, k;\n\t"
+      "sub.f16x2 h, h, c;\n\tmul.f16x2 h, h, s;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %2, k;\n\t}"
+      : "=r"(p0), "=r"(p1), "=r"(p2) : "f"(a), "f"(b));
 }
 // Two values as three e4m3 codes each, every one 2^-4 of the one before.
 __device__ __forceinline__ void split3(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
@@ -570,7 +582,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     constexpr bool kRegs = NU == 1;
     constexpr float kSlack = C::kSlack, kLift = C::kLift;
     float mr[kRegs ? UN : 1] = {}, qm[kRegs ? UN : 1] = {};
-    auto refs = [&](int u, int i) { return kRegs ? mr[kRegs ? i : 0] : ctl->ref[row_of(u) + i]; };
+    auto refs = [&](int u, int i) -> uint64_t {  // of rows i, i + 1
+      return kRegs ? pair(mr[kRegs ? i : 0], mr[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(ctl->ref + row_of(u) + i);
+    };
 #pragma unroll 1
     for (uint32_t it = 0;; ++it) {
       const Item& x_ = item_at(it);
@@ -583,15 +597,17 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       float vn = 0.f;
 #pragma unroll
       for (int r = 0; r < NU * UN; ++r) l[r] = 0.f;
-      if (tid < TM) ctl->ref[tid] = -INFINITY;
+      if (tid < TM) ctl->ref[tid] = kNoRef;
       if (kRegs) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-          mr[kRegs ? i : 0] = -INFINITY;
+          mr[kRegs ? i : 0] = kNoRef;
           if (F8) qm[kRegs ? i : 0] = qmul[row_of(0) + i];
         }
       }
-      auto muls = [&](int u, int i) { return kRegs ? qm[kRegs ? i : 0] : qmul[row_of(u) + i]; };
+      auto muls = [&](int u, int i) -> uint64_t {
+        return kRegs ? pair(qm[kRegs ? i : 0], qm[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(qmul + row_of(u) + i);
+      };
       softmax_sync();
 #pragma unroll 1
       for (int n = 0; n < n_here; ++n, ++ti) {
@@ -614,7 +630,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         const bool open = have == FULL_MASK && key0 + kTK - 1 <= pmin && (A.window <= 0 || key0 > pmax - A.window);
         const bool mine = (have >> lane) & 1;
         float s[NU * UN];
-        bool over = F8 && mine && vs > vn;
+        float most = -INFINITY;  // over the references
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           const int r0 = row_of(u);
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               ld_n<UN>(col, x);
               wait_ld_n<UN>(x);
 #pragma unroll
-              for (int i = 0; i < UN; ++i) x[i] *= A.c;
+              for (int i = 0; i < UN; i += 2) unpair(mul2(pair(x[i], x[i + 1]), pair(A.c, A.c)), x[i], x[i + 1]);
             } else {
               float y[UN], z[UN];
               ld_n<UN>(col, x);
@@ -635,7 +651,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               wait_ld_n<UN>(y);
               wait_ld_n<UN>(z);
 #pragma unroll
-              for (int i = 0; i < UN; ++i) x[i] = fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, x[i])) * (ks * muls(u, i));
+              for (int i = 0; i < UN; i += 2) {
+                const uint64_t lo = fma2(pair(z[i], z[i + 1]), pair(0x1p-4f, 0x1p-4f), pair(y[i], y[i + 1]));
+                const uint64_t all = fma2(lo, pair(0x1p-4f, 0x1p-4f), pair(x[i], x[i + 1]));
+                unpair(mul2(all, mul2(pair(ks, ks), muls(u, i))), x[i], x[i + 1]);
+              }
             }
             if (!open) {
 #pragma unroll
@@ -645,10 +665,14 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               }
             }
 #pragma unroll
-            for (int i = 0; i < UN; ++i) over |= x[i] > refs(u, i) + kSlack;
+            for (int i = 0; i < UN; i += 2) {
+              float a, b;
+              unpair(add2(pair(x[i], x[i + 1]), refs(u, i)), a, b);
+              most = max3(most, a, b);
+            }
           }
         }
-        if (softmax_any(over)) {  // some reference moves: to the tile's maxima
+        if (softmax_any(most > kSlack || (F8 && mine && vs > vn))) {  // some reference moves: to the tile's maxima
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
             if (row_of(u) < R) {
@@ -678,8 +702,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           if (tid < (R + UN - 1) / UN * UN) {
             const int r = tid;
             const float top = fmaxf(fmaxf(ctl->red[0][r], ctl->red[1][r]), fmaxf(ctl->red[2][r], ctl->red[3][r]));
-            const float m = ctl->ref[r], m1 = top > m + kSlack ? top : m;
-            ctl->fac[r] = m1 == m ? 1.f : ex2(m - m1);
+            const float m = ctl->ref[r], m1 = top + m > kSlack ? -top : m;  // negated
+            ctl->fac[r] = m1 == m ? 1.f : ex2(m1 - m);
             ctl->ref[r] = m1;
           }
           if (n > 0) {  // the products so far
@@ -718,30 +742,32 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
         // the weights of tile ti - 2 have been used: its products were issued before these scores
         const uint32_t pd = sb + C::kOffP + (ti & 1) * C::kP + key * 16;
-        // relative V scale (a NaN scale of an unseen key stays out)
+        // relative V scale; no weight exceeds 2^8, and an infinite scale makes a NaN
         const float f = F8 ? vs * __frcp_rn(fmaxf(vn, 0x1p-126f)) * kLift : kLift;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           const int r0 = row_of(u);
           if (r0 < R) {
-            float p[UN];
-#pragma unroll
-            for (int i = 0; i < UN; ++i) {
-              const float x = s[u * UN + i], m = refs(u, i);
-              p[i] = ex2(x - (m == -INFINITY ? 0.f : m));
-              l[u * UN + i] += p[i];
-              if (F8) {
-                p[i] = x == -INFINITY ? 0.f : p[i] * f;
-                p[i] = p[i] <= 448.f ? p[i] : NAN;  // never above, but an infinite scale
-              } else {
-                p[i] *= f;
-              }
-            }
             uint32_t w[3][UN / 2];
 #pragma unroll
-            for (int i = 0; i < UN / 2; ++i) {
-              if (!F8) split2<DT>(p[2 * i], p[2 * i + 1], w[0][i], w[1][i]);
-              else split3(p[2 * i], p[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+            for (int i = 0; i < UN; i += 2) {
+              const float* const x = s + u * UN + i;
+              float p[2];
+              unpair(add2(pair(x[0], x[1]), refs(u, i)), p[0], p[1]);
+              p[0] = ex2(p[0]);
+              p[1] = ex2(p[1]);
+              const uint64_t pp = pair(p[0], p[1]);
+              unpair(add2(pair(l[u * UN + i], l[u * UN + i + 1]), pp), l[u * UN + i], l[u * UN + i + 1]);
+              unpair(mul2(pp, pair(f, f)), p[0], p[1]);
+              if (F8) {
+                if (!open) {  // a NaN scale of an unseen key stays out
+                  p[0] = x[0] == -INFINITY ? 0.f : p[0];
+                  p[1] = x[1] == -INFINITY ? 0.f : p[1];
+                }
+                split3_weights(pair(p[0], p[1]), w[0][i / 2], w[1][i / 2], w[2][i / 2]);
+              } else {
+                split2<DT>(p[0], p[1], w[0][i / 2], w[1][i / 2]);
+              }
             }
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
@@ -787,7 +813,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           if (lane % (32 / UN) == 0) ctl->sum[it & 1][wk][row_of(u) + lane / (32 / UN)] = v[0];
         }
       }
-      if (tid < TM) ctl->end_ref[it & 1][tid] = ctl->ref[tid];
+      if (tid < TM) ctl->end_ref[it & 1][tid] = ctl->ref[tid] == kNoRef ? -INFINITY : -ctl->ref[tid];
       if (tid == 0) ctl->unit[it & 1] = (F8 ? vn : 1.f) * (1.f / C::kLift);
       arrive(&ctl->sum_full[it & 1]);
       if (flags & 4) break;
