@@ -142,55 +142,41 @@ __device__ __forceinline__ long long share(long long a, int b, int c) {
   return a * b / c;
 }
 
-// This CTA's run of the line (all NT threads; sh: NT / 32 + 2 words of shared
-// memory, free again afterwards).  Runs are at least min_run tiles on average.
-// False: this CTA has none.  total, ctas, u1: tiles in the line, runs, this run's end.
-template <int TM, int TK, int NT>
-__device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_run, long long* sh,
-                                         Cursor<TM, TK>& c, long long& total, int& ctas, long long& u1) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int B = A.kv.B;
-  const long long mine0 = tid < B ? seq_tiles<TM, TK>(A, cls, tid) : 0;
-  long long v = mine0;
-  for (int b = tid + NT; b < B; b += NT) v += seq_tiles<TM, TK>(A, cls, b);
+// This CTA's run of the line.  Every warp finds it by itself, a lane adding up some neighbouring
+// sequences: nobody waits for anybody.  Runs are at least min_run tiles on average.  False: this CTA has
+// none.  total, ctas, u1: tiles in the line, runs, this run's end.
+template <int TM, int TK>
+__device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_run, Cursor<TM, TK>& c, long long& total,
+                                         int& ctas, long long& u1) {
+  const int lane = threadIdx.x & 31, B = A.kv.B, per = (B + 31) >> 5, b0 = lane * per;
+  long long mine = 0;
+#pragma unroll 4
+  for (int i = 0; i < per; ++i)
+    if (b0 + i < B) mine += seq_tiles<TM, TK>(A, cls, b0 + i);
+  long long inc = mine;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
-  if (lane == 0) sh[warp] = v;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < NT / 32; ++i) total += sh[i];
-  __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(FULL_MASK, inc, o);
+    if (lane >= o) inc += y;
+  }
+  total = __shfl_sync(FULL_MASK, inc, 31);
   ctas = (int)min((long long)gridDim.x, total < (1ll << 31) ? (long long)(((uint32_t)total + min_run - 1) / min_run) : total);
   if ((int)blockIdx.x >= ctas) return false;
   const long long u0 = share(total, blockIdx.x, ctas);
   u1 = share(total, blockIdx.x + 1, ctas);
-  long long base = 0;
-  for (int b0 = 0;; b0 += NT) {  // the sequence that holds tile u0 (there is one: u0 < total)
-    const int b = b0 + tid;
-    const long long w = b0 == 0 ? mine0 : (b < B ? seq_tiles<TM, TK>(A, cls, b) : 0);
-    long long inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(FULL_MASK, inc, o);
-      if (lane >= o) inc += y;
+  // the sequence that holds tile u0 (there is one: u0 < total)
+  long long off = u0 - (inc - mine);
+  const int src = __ffs(__ballot_sync(FULL_MASK, off >= 0 && off < mine)) - 1;
+  int b = b0;
+  if (lane == src) {
+    for (;; ++b) {
+      const long long w = seq_tiles<TM, TK>(A, cls, b);
+      if (off < w) break;
+      off -= w;
     }
-    if (lane == 31) sh[warp] = inc;
-    __syncthreads();
-    long long before = base;
-    for (int i = 0; i < warp; ++i) before += sh[i];
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) base += sh[i];
-    if (w > 0 && before + inc - w <= u0 && u0 < before + inc) {
-      sh[NT / 32] = b;
-      sh[NT / 32 + 1] = u0 - (before + inc - w);
-    }
-    __syncthreads();
-    if (u0 < base) break;
   }
-  c.seek(A, cls, (int)sh[NT / 32], sh[NT / 32 + 1]);
+  c.seek(A, cls, __shfl_sync(FULL_MASK, b, src), __shfl_sync(FULL_MASK, off, src));
   c.left = u1 - u0;
-  __syncthreads();
   return true;
 }
 

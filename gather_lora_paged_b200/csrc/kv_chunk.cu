@@ -58,11 +58,11 @@ struct Cfg {
 template <int S>
 struct Ctl {
   uint64_t kv_full[S], kv_empty[S], q_full, q_empty, item_full[kItems], item_empty[kItems], rows_full[kItems];
-  uint64_t s_full[2], p_full[2][2], o_full[2], fin;  // p_full[q tile][half of the keys]
+  uint64_t s_full[2], p_full[2][2], o_full[2], tmem_full, fin;  // p_full[q tile][half of the keys]
   Item item[kItems];
   uint32_t tmem;
   int dead;                    // a wait gave up: nobody waits any more
-  uint32_t mask[kMeta][4];     // keys of a tile that are there
+  alignas(16) uint32_t mask[kMeta][4];  // keys of a tile that are there
 };
 
 __device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
@@ -133,44 +133,39 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
 
   griddep_launch();  // the join's CTAs may take their places (they wait for this grid's end)
   if (tid == 0) split->n = 0;
+  if (warp == 12) {
+    for (int i = lane; i < S; i += 32) {
+      bar_init(&ctl->kv_full[i], 128 + (F8 ? 128 : 4));
+      bar_init(&ctl->kv_empty[i], 1);
+    }
+    if (lane < kItems) {
+      bar_init(&ctl->item_full[lane], 1);
+      bar_init(&ctl->item_empty[lane], 2);
+      bar_init(&ctl->rows_full[lane], 128);
+    }
+    if (lane < 2) {
+      bar_init(&ctl->s_full[lane], 1);
+      bar_init(&ctl->p_full[lane][0], 128);
+      bar_init(&ctl->p_full[lane][1], 128);
+      bar_init(&ctl->o_full[lane], 1);
+    }
+    if (lane == 0) {
+      bar_init(&ctl->q_full, 256);
+      bar_init(&ctl->q_empty, 1);
+      bar_init(&ctl->tmem_full, 32);
+      bar_init(&ctl->fin, 1);
+      ctl->dead = 0;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   Cursor<kTM, kTK> c;
   long long total, u1;
   int ctas;
-  if (!find_run<kTM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) {
+  if (!find_run<kTM, kTK>(A, cls, kMinRun, c, total, ctas, u1)) {
     griddep_wait();
     return;
   }
-
-  if (warp == 12) {
-    if (lane == 0) {
-      for (int i = 0; i < S; ++i) {
-        bar_init(&ctl->kv_full[i], 128 + (F8 ? 128 : 4));
-        bar_init(&ctl->kv_empty[i], 1);
-      }
-      bar_init(&ctl->q_full, 256);
-      bar_init(&ctl->q_empty, 1);
-      for (int i = 0; i < kItems; ++i) {
-        bar_init(&ctl->item_full[i], 1);
-        bar_init(&ctl->item_empty[i], 2);
-        bar_init(&ctl->rows_full[i], 128);
-      }
-      for (int i = 0; i < 2; ++i) {
-        bar_init(&ctl->s_full[i], 1);
-        bar_init(&ctl->p_full[i][0], 128);
-        bar_init(&ctl->p_full[i][1], 128);
-        bar_init(&ctl->o_full[i], 1);
-      }
-      bar_init(&ctl->fin, 1);
-      ctl->dead = 0;
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncwarp();
-    tmem_alloc(&ctl->tmem, 512);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  __syncthreads();  // the barriers are there
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
   // An item's entry.  It is written again for item it + 4, once both softmax groups are through with
   // this one; all others have read it by then.
@@ -201,6 +196,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       __syncwarp();
     } else if (warp == 12) {
       // ---------------------------------------------------------- MMA issuer
+      tmem_alloc(&ctl->tmem, 512);
+      __syncwarp();
+      const uint32_t tmem = ctl->tmem;
+      arrive(&ctl->tmem_full);
       const uint32_t fmt = MT == SLORA_BF16 ? 1u : 0u;
       const uint32_t id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
       const uint32_t id_s = id0 | ((uint32_t)kTK >> 3) << 17, id_o = id0 | (1u << 16) | ((uint32_t)D >> 3) << 17;  // V: MN-major
@@ -456,6 +455,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int wg = warp >> 2;
+    wait(&ctl->tmem_full, 0);
+    const uint32_t tmem = ctl->tmem;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + wg * 128, to = tmem + lanes + 256 + wg * 128;
     uint32_t sn = 0, on = 0, ti = 0;
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(ctl->tmem, 512);
   griddep_wait();  // for kv_decode.cu's grid: who waits for this one waits for both
 }
 
@@ -694,7 +695,7 @@ cudaError_t run_chunk(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream
   using C = Cfg<FMT, D>;
   static std::atomic<bool> sized[64];
   constexpr int bytes = 1024 + C::kOffCtl + (int)sizeof(Ctl<C::kSlots>);
-  static_assert(bytes <= 232448, "shared memory");
+  static_assert(bytes <= 232448 && C::kOffCtl % 16 == 0, "shared memory");
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_chunk<DT, FMT, D>), bytes, sized);
   if (e != cudaSuccess) return e;
   return launch_behind(k_kv_chunk<DT, FMT, D>, dim3(sm_count), kNT, bytes, st, A, cls);

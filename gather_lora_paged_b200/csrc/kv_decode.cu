@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 
   griddep_launch();  // the join's CTAs may take their places (they wait for this grid's end)
   if (tid == 0) split->n = 0;
-  if (warp == 12) {  // behind find_run's barriers when somebody needs them
+  if (warp == 12) {
     for (int i = lane; i < S; i += 32) {
       bar_init(&ctl->kv_full[i], 128 + 4);
       bar_init(&ctl->kv_empty[i], 1);
@@ -262,11 +262,12 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
   Cursor<TM, kTK> c;
   long long total, u1;
   int ctas;
-  if (!find_run<TM, kTK, kNT>(A, cls, kMinRun, reinterpret_cast<long long*>(smem), c, total, ctas, u1)) {
+  if (!find_run<TM, kTK>(A, cls, kMinRun, c, total, ctas, u1)) {
     if (blockIdx.x == 0) kv_record_bad(P, A.max_rows, tid, kNT);
     return;
   }
 
+  __syncthreads();  // the barriers are there
   const int n_tiles = (int)c.left;
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
   auto tmem_at = [&]() -> uint32_t {  // for those who do not allocate it
@@ -922,7 +923,7 @@ template <int DT, int FMT, int D, int TM>
 cudaError_t run_decode(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream_t st) {
   using C = Cfg<FMT, D, TM>;
   constexpr int bytes = 1024 + C::kOffCtl + (int)sizeof(Ctl<TM, C::kSlots>);
-  static_assert(bytes <= 232448, "shared memory");
+  static_assert(bytes <= 232448 && C::kOffCtl % 16 == 0, "shared memory");
   static std::atomic<bool> sized[64];
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_decode<DT, FMT, D, TM>), bytes, sized);
   if (e != cudaSuccess) return e;
