@@ -292,7 +292,7 @@ __device__ __noinline__ void redo_row(const KvAttnDev& A, int b, int h, const ui
 
 // Joins the partials of the item that starts in run `run` of a kernel's `ctas` and ends in a
 // later one: weights exp2(m_i - max m), in key order.  A warp per row.
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 256;
 template <int DT, int D, int TM>
 __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* workspace, int run, int ctas) {
   constexpr int E = D / 32;
@@ -304,7 +304,7 @@ __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* worksp
   kv_seq(A.kv, sp.b, A.max_rows, s);
   const int r_item = sp.rt * TM, R = min(s.n * A.G - r_item, TM);
   auto at = [&](int i) { return parts + (size_t)(i == 0 ? sp.slot : 2 * (run + i)) * slot_floats(TM, D); };
-  for (int r = blockIdx.y * 4 + warp; r < R; r += gridDim.y * 4) {
+  for (int r = blockIdx.y * (kCombineThreads / 32) + warp; r < R; r += gridDim.y * (kCombineThreads / 32)) {
     float top = -INFINITY;
     for (int i = lane; i < sp.n; i += 32) top = fmaxf(top, at(i)[(size_t)TM * D + r]);
 #pragma unroll

@@ -703,7 +703,8 @@ cudaError_t run_chunk(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream
 
 template <int DT, int D>
 cudaError_t run_join(const KvAttnDev& A, int TM, bool chunks, int sm_count, cudaStream_t st) {
-  const dim3 grid(chunks ? 2 * sm_count : sm_count, chunks ? kTM / 16 : (TM + 15) / 16);
+  // a row per warp, two where there are row tiles of 256
+  const dim3 grid(chunks ? 2 * sm_count : sm_count, chunks ? kTM / 16 : TM / 8);
   if (TM == 8) return launch_behind(k_kv_join<DT, D, 8>, grid, kCombineThreads, 0, st, A, sm_count);
   if (TM == 16) return launch_behind(k_kv_join<DT, D, 16>, grid, kCombineThreads, 0, st, A, sm_count);
   if (TM == 32) return launch_behind(k_kv_join<DT, D, 32>, grid, kCombineThreads, 0, st, A, sm_count);

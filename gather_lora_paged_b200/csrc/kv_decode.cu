@@ -20,7 +20,7 @@
 //   warps 8..11 copy K and V rows into a ring of slots (K or V of a tile), 32 keys
 //               each; the copies signal the slot's barrier when they land;
 //   warp 13     the run's items, for all others;
-//   warp 14     q of the items ahead, as the N side of S^T, and the rows' positions;
+//   warps 14, 15  q of the items ahead, as the N side of S^T, and the rows' positions;
 //   warp 12     issues S^T of tile i + 1, then O^T of tile i;
 //   warps 0..7  the softmax: a thread owns a key and half of the rows, reads its scores from TMEM
 //               and writes its weights to shared memory as the N side of O^T;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       bar_init(&ctl->kv_empty[i], 1);
     }
     if (lane < 2) {
-      bar_init(&ctl->q_full[lane], 64);
+      bar_init(&ctl->q_full[lane], 128);
       bar_init(&ctl->q_empty[lane], 1);
       bar_init(&ctl->s_full[lane], 1);
       bar_init(&ctl->p_full[lane], 256);
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     if (lane < kItems) {
       bar_init(&ctl->item_full[lane], 1);
       bar_init(&ctl->item_empty[lane], 1);
-      bar_init(&ctl->rows_full[lane], 32);
+      bar_init(&ctl->rows_full[lane], 64);
     }
     if (lane == 0) {
       bar_init(&ctl->tmem_full, 32);
@@ -401,14 +401,15 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp >= 14) {
       // ----------------------------------------------------- q, positions
+      const int qw = warp - 14;
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
         const Item& x = item_at(it);
         const int R = x.R, r_item = x.rt * TM, row0 = x.row0, hq0 = x.h * A.G, last = x.flags & 4;
         const uint32_t dst = sb + C::kOffQ + (it & 1) * C::kQ;
-        for (int r = lane; r < C::kRows16; r += 32)
+        for (int r = lane + 32 * qw; r < C::kRows16; r += 64)
           ctl->pos[it % kItems][r] = r < R ? x.first + token_of(A, r_item + r) : -1;
         wait(&ctl->q_empty[it & 1], ((it >> 1) & 1) ^ 1);
         auto row_of = [&](int r) -> const uint16_t* {
@@ -418,47 +419,53 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         const int rows = (R + 15) / 16 * 16;
         if (!F8) {
           constexpr int QL = D / 8, QR = 32 / QL;  // lanes per row, rows per pass
-          for (int r = lane / QL; r < rows; r += QR)
+          for (int r = qw * QR + lane / QL; r < rows; r += 2 * QR)
             cp16(dst + place<128>(C::kQRows, r, lane % QL), r < R ? row_of(r) + (lane % QL) * 8 : A.q, r < R);
         } else {
-          constexpr int QL = D / 4, QR = 32 / QL;  // four elements a lane
-          const int e0 = (lane % QL) * 4;
+          constexpr int QL = D / 16, QR = 32 / QL;  // 16 elements a lane
+          const int ch = lane % QL;
+          uint4 v[2];
+          auto load = [&](int r) {
+            v[0] = v[1] = make_uint4(0, 0, 0, 0);
+            if (r < R) {
+              const uint4* const src = reinterpret_cast<const uint4*>(row_of(r)) + 2 * ch;
+              v[0] = __ldg(src);
+              v[1] = __ldg(src + 1);
+            }
+          };
+          int r = qw * QR + lane / QL;
+          load(r);
 #pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 4 * QR) {
-            uint2 v[4];
+          for (; r - lane / QL < rows; r += 2 * QR) {
+            const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+            load(r + 2 * QR);
+            float f[16];
+            uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + k * QR + lane / QL;
-              v[k] = r < R ? __ldg(reinterpret_cast<const uint2*>(row_of(r) + e0)) : make_uint2(0, 0);
+            for (int i = 0; i < 8; ++i) {
+              up2<DT>(x[i], f[2 * i], f[2 * i + 1]);
+              top = max(top, max(__float_as_uint(f[2 * i]) & 0x7fffffffu, __float_as_uint(f[2 * i + 1]) & 0x7fffffffu));
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + k * QR + lane / QL;
-              float f[4];
-              up2<DT>(v[k].x, f[0], f[1]);
-              up2<DT>(v[k].y, f[2], f[3]);
-              uint32_t top = 0;
+            for (int o = QL / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+            const int e = min(max((int)(top >> 23) - 127, -100), 127);
+            const float up = __int_as_float((134 - e) << 23);  // 2^(7 - e)
+            uint32_t p[3][4] = {};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+            for (int i = 0; i < 16; i += 2) {
+              // an infinity or a NaN becomes a NaN code (satfinite would make the infinity a number)
+              const float a = f[i] * up, b = f[i + 1] * up;
+              uint32_t h[3];
+              split3(a - a == 0.f ? a : NAN, b - b == 0.f ? b : NAN, h[0], h[1], h[2]);
 #pragma unroll
-              for (int o = QL / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
-              const int e = min(max((int)(top >> 23) - 127, -100), 127);
-              const float up = __int_as_float((134 - e) << 23);  // 2^(7 - e)
-              uint32_t p[3] = {0, 0, 0};
-#pragma unroll
-              for (int i = 0; i < 4; i += 2) {
-                // an infinity or a NaN becomes a NaN code (satfinite would make the infinity a number)
-                const float a = f[i] * up, b = f[i + 1] * up;
-                uint32_t h[3];
-                split3(a - a == 0.f ? a : NAN, b - b == 0.f ? b : NAN, h[0], h[1], h[2]);
-#pragma unroll
-                for (int q = 0; q < 3; ++q) p[q] |= h[q] << (8 * i);
-              }
-              const int col = r / 16 * 48 + r % 16;
+              for (int q = 0; q < 3; ++q) p[q][i / 4] |= h[q] << (8 * (i & 2));
+            }
+            const int col = r / 16 * 48 + r % 16;
+            if (r < rows) {
 #pragma unroll
               for (int q = 0; q < 3; ++q)
-                st_shared4(dst + place<W>(C::kQRows, col + q * 16, (lane % QL) >> 2) + (lane & 3) * 4, p[q]);
-              if (lane % QL == 0) ctl->qmul[it % kItems][r] = A.c * __int_as_float((120 + e) << 23);
+                st_shared16(dst + place<W>(C::kQRows, col + q * 16, ch), p[q][0], p[q][1], p[q][2], p[q][3]);
+              if (ch == 0) ctl->qmul[it % kItems][r] = A.c * __int_as_float((120 + e) << 23);
             }
           }
           fence_async_smem();
@@ -469,8 +476,6 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         if (last) break;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 15) {
-      if (blockIdx.x == 0) kv_record_bad(P, A.max_rows, lane, 32);
     } else if (warp == 12) {
       // ---------------------------------------------------------- MMA issuer
       tmem_alloc(&ctl->tmem, C::kTmem);
@@ -823,6 +828,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     // ------------------------------------------- the rows of an item, or their partials
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int wl = warp - 16, tl = tid - 512;
+    if (blockIdx.x == 0) kv_record_bad(P, A.max_rows, tl, 128);
     const uint32_t tmem = tmem_at(), ts = tmem + ((uint32_t)(wl * 32) << 16);
     const int d = D == 128 ? tl : wl * 16 + (lane & 15);
     const bool writes = D == 128 || lane < 16;
