@@ -4,11 +4,12 @@
 //
 // The rows of a kv head are the n * G pairs (token, head of the group), in row
 // tiles of TM.  A work item is (sequence, kv head, row tile); its keys come in
-// tiles of TK, and the tiles of all items, laid out in one line, are cut into
-// equal runs, one per CTA, so that ragged lengths and a single long sequence
-// keep every SM equally busy.  An item inside one run is finished there; one that
+// tiles of TK.  All items, laid out in one line, are cut into equal runs, one per CTA, so
+// that ragged lengths and a single long sequence keep every SM equally busy.  An item is as long there as
+// its tiles and a lead of E units, for what it costs beside them (q, the first maximum, its
+// outputs).  An item inside one run is finished there; one that
 // crosses runs leaves (max, sum, unnormalised row) partials, at most two per
-// CTA, and k_kv_combine joins them in key order.
+// CTA, and k_kv_join joins them in key order.
 #pragma once
 
 #include <atomic>
@@ -73,28 +74,29 @@ __device__ __forceinline__ bool takes(const KvAttnDev& A, RowClass cls, int b, K
   const int64_t R = (int64_t)s.n * A.G;
   return R > cls.lo && R <= cls.hi;
 }
-// Tiles of all items of sequence b.
-template <int TM, int TK>
-__device__ __forceinline__ long long seq_tiles(const KvAttnDev& A, RowClass cls, int b) {
+// Units of all items of sequence b: the lead of an item and its tiles.
+template <int TM, int TK, int E>
+__device__ __forceinline__ long long seq_units(const KvAttnDev& A, RowClass cls, int b) {
   KvSeq s;
   if (!takes(A, cls, b, s)) return 0;
   const int RT = cdiv_i(s.n * A.G, TM);
   long long u = 0;
   for (int rt = 0; rt < RT; ++rt) {
     const Span x = span_of<TM, TK>(A, s, rt);
-    u += x.t1 - x.t0;
+    u += E + x.t1 - x.t0;
   }
   return u * A.kv.H;
 }
 
-// A place in the line of tiles.
-template <int TM, int TK>
+// A place in the line.
+template <int TM, int TK, int E>
 struct Cursor {
   KvSeq s;
   Span x;
-  int b, h, rt, RT, tile;
-  long long left;  // tiles of this CTA from here on
+  int b, h, rt, RT, at;  // at: units of the item before this place
+  long long left;        // units of this run from here on
 
+  __device__ int size() const { return E + x.t1 - x.t0; }
   __device__ void seek(const KvAttnDev& A, RowClass cls, int b_, long long off) {
     b = b_;
     takes(A, cls, b, s);
@@ -102,36 +104,32 @@ struct Cursor {
     long long per = 0;
     for (rt = 0; rt < RT; ++rt) {
       x = span_of<TM, TK>(A, s, rt);
-      per += x.t1 - x.t0;
+      per += size();
     }
     h = off < (1ll << 31) && per < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
     off -= h * per;
     for (rt = 0;; ++rt) {
       x = span_of<TM, TK>(A, s, rt);
-      if (off < x.t1 - x.t0) break;
-      off -= x.t1 - x.t0;
+      if (off < size()) break;
+      off -= size();
     }
-    tile = x.t0 + (int)off;
+    at = (int)off;
   }
-  __device__ bool last_of_item() const { return tile + 1 == x.t1; }
-  __device__ bool next(const KvAttnDev& A, RowClass cls) {  // false: the run is over
-    if (--left <= 0) return false;
-    if (++tile < x.t1) return true;
+  __device__ bool next(const KvAttnDev& A, RowClass cls) {  // to the next item; false: no tile of it is in the run
+    left -= size() - at;
+    if (left <= E) return false;
+    at = 0;
     if (++rt == RT) {
       rt = 0;
       if (++h == A.kv.H) {
         h = 0;
         do ++b;
         while (b < A.kv.B && !takes(A, cls, b, s));
-        if (b >= A.kv.B) {  // cannot be: the run ends first
-          left = 0;
-          return false;
-        }
+        if (b >= A.kv.B) return false;  // cannot be: the run ends first
         RT = cdiv_i(s.n * A.G, TM);
       }
     }
     x = span_of<TM, TK>(A, s, rt);
-    tile = x.t0;
     return true;
   }
 };
@@ -143,16 +141,16 @@ __device__ __forceinline__ long long share(long long a, int b, int c) {
 }
 
 // This CTA's run of the line.  Every warp finds it by itself, a lane adding up some neighbouring
-// sequences: nobody waits for anybody.  Runs are at least min_run tiles on average.  False: this CTA has
-// none.  total, ctas, u1: tiles in the line, runs, this run's end.
-template <int TM, int TK>
-__device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_run, Cursor<TM, TK>& c, long long& total,
-                                         int& ctas, long long& u1) {
+// sequences: nobody waits for anybody.  Runs are at least E + min_tiles units, so that each has a tile.
+// False: this CTA has none.  total, ctas, u1: units in the line, runs, this run's end.
+template <int TM, int TK, int E>
+__device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_tiles, Cursor<TM, TK, E>& c,
+                                         long long& total, int& ctas, long long& u1) {
   const int lane = threadIdx.x & 31, B = A.kv.B, per = (B + 31) >> 5, b0 = lane * per;
   long long mine = 0;
 #pragma unroll 4
   for (int i = 0; i < per; ++i)
-    if (b0 + i < B) mine += seq_tiles<TM, TK>(A, cls, b0 + i);
+    if (b0 + i < B) mine += seq_units<TM, TK, E>(A, cls, b0 + i);
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -160,17 +158,18 @@ __device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int m
     if (lane >= o) inc += y;
   }
   total = __shfl_sync(FULL_MASK, inc, 31);
-  ctas = (int)min((long long)gridDim.x, total < (1ll << 31) ? (long long)(((uint32_t)total + min_run - 1) / min_run) : total);
+  ctas = (int)min((long long)gridDim.x, total < (1ll << 31) ? (long long)((uint32_t)total / (uint32_t)(E + min_tiles)) : total);
+  ctas = max(ctas, total > 0 ? 1 : 0);
   if ((int)blockIdx.x >= ctas) return false;
   const long long u0 = share(total, blockIdx.x, ctas);
   u1 = share(total, blockIdx.x + 1, ctas);
-  // the sequence that holds tile u0 (there is one: u0 < total)
+  // the sequence that holds unit u0 (there is one: u0 < total)
   long long off = u0 - (inc - mine);
   const int src = __ffs(__ballot_sync(FULL_MASK, off >= 0 && off < mine)) - 1;
   int b = b0;
   if (lane == src) {
     for (;; ++b) {
-      const long long w = seq_tiles<TM, TK>(A, cls, b);
+      const long long w = seq_units<TM, TK, E>(A, cls, b);
       if (off < w) break;
       off -= w;
     }
@@ -190,8 +189,9 @@ struct Item {
   int pad;
 };
 
-template <int TM, int TK>
-__device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK>& c) {
+template <int TM, int TK, int E>
+__device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK, E>& c) {
+  const int end = (int)min((long long)c.size(), c.at + c.left), first = max(c.at - E, 0);
   Item x;
   x.b = c.b;
   x.h = c.h;
@@ -201,18 +201,18 @@ __device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK>
   x.first = c.s.len - c.s.n;
   x.lo = c.x.lo;
   x.hi = c.x.hi;
-  x.tile = c.tile;
-  x.n_tiles = (int)min((long long)(c.x.t1 - c.tile), c.left);
-  x.flags = (c.tile == c.x.t0 ? 1 : 0) | (c.tile + x.n_tiles == c.x.t1 ? 2 : 0) | (c.left == x.n_tiles ? 4 : 0);
+  x.tile = c.x.t0 + first;
+  x.n_tiles = end - E - first;
+  x.flags = (first == 0 ? 1 : 0) | (end == c.size() ? 2 : 0) | (c.left - (end - c.at) <= E ? 4 : 0);
   x.pad = 0;
   return x;
 }
 
 // Partials of an item whose first tile is in this run (slot: this CTA's) and
-// whose last tile is number end - 1 of the line.
+// whose last one is unit end - 1 of the line.
 __device__ __forceinline__ void note_split(Split* sp, int b, int h, int rt, int slot, long long end, long long total,
                                            int ctas) {
-  // the run of tile end - 1
+  // the run of unit end - 1
   const long long x = end * ctas + total - 1, last = (x < (1ll << 32) ? (uint32_t)x / (uint32_t)total : x / total) - 1;
   sp->b = b;
   sp->h = h;

@@ -38,6 +38,7 @@ constexpr int kNT = 512;
 constexpr int kTM = 256;      // rows per item
 constexpr int kTK = kKvTile;  // keys per tile
 constexpr int kMinRun = 2;
+constexpr int kLead = 2;      // an item's lead: q and the outputs cost about two tiles
 constexpr int kItems = 4;     // items that are known ahead
 constexpr int kMeta = 8;      // tiles whose scales and masks are kept
 constexpr float kSlack = 8.f; // log2 of the largest weight
@@ -158,10 +159,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  Cursor<kTM, kTK> c;
+  Cursor<kTM, kTK, kLead> c;
   long long total, u1;
   int ctas;
-  if (!find_run<kTM, kTK>(A, cls, kMinRun, c, total, ctas, u1)) {
+  if (!find_run<kTM, kTK, kLead>(A, cls, kMinRun, c, total, ctas, u1)) {
     griddep_wait();
     return;
   }
@@ -184,13 +185,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         for (uint32_t it = 0;; ++it) {
           const Item x = item_of(A, c);
           if ((x.flags & 3) == 1)
-            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.x.t1 - c.tile), total, ctas);
+            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
           wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
           ctl->item[it % kItems] = x;
           arrive(&ctl->item_full[it % kItems]);
-          c.tile += x.n_tiles - 1;
-          c.left -= x.n_tiles - 1;
-          if (!c.next(A, cls)) break;
+          if ((x.flags & 4) || !c.next(A, cls)) break;
         }
       }
       __syncwarp();

@@ -259,16 +259,16 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  Cursor<TM, kTK> c;
+  constexpr int E = TM <= 16 ? 1 : 2;  // an item's lead: measured 0.5 to 1.5 tiles
+  Cursor<TM, kTK, E> c;
   long long total, u1;
   int ctas;
-  if (!find_run<TM, kTK>(A, cls, kMinRun, c, total, ctas, u1)) {
+  if (!find_run<TM, kTK, E>(A, cls, kMinRun, c, total, ctas, u1)) {
     if (blockIdx.x == 0) kv_record_bad(P, A.max_rows, tid, kNT);
     return;
   }
 
   __syncthreads();  // the barriers are there
-  const int n_tiles = (int)c.left;
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
   auto tmem_at = [&]() -> uint32_t {  // for those who do not allocate it
     wait(&ctl->tmem_full, 0);
@@ -301,17 +301,20 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 #pragma unroll
       for (int k = 0; k < NSW; ++k) swz[k] = place<W>(kTK, k * RPI + jl, cl) - k * RPI * W;
       // the item whose tiles are looked up: the first one is known here
+      const Item x0 = item_of(A, c);
       uint32_t it = 1;
-      int left = (int)min((long long)(c.x.t1 - c.tile), c.left), j = c.tile * kTK + key, lo = c.x.lo, hi = c.x.hi, b = c.b,
-          off = c.h * P.pt;
+      int left = x0.n_tiles, j = x0.tile * kTK + key, lo = x0.lo, hi = x0.hi, b = x0.b, off = x0.h * P.pt, last = x0.flags & 4;
+      int todo = 0;  // tiles looked up and not yet copied
       int pg[3], at[3], sq[3];  // page and place in it (-1: no such key) of this lane's key, three tiles
-      auto fetch = [&](int i, int ti) {
+      auto fetch = [&](int i) {
         at[i] = -1;
         pg[i] = 0;
-        if (ti < n_tiles) {
+        if (left > 0 || !last) {
+          ++todo;
           if (left == 0) {
             const Item& x = item_at(it++);
             left = x.n_tiles;
+            last = x.flags & 4;
             j = x.tile * kTK + key;
             lo = x.lo;
             hi = x.hi;
@@ -328,12 +331,12 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           --left;
         }
       };
-      fetch(0, 0);
-      fetch(1, 1);
+      fetch(0);
+      fetch(1);
       uint32_t slot = 0, phase = 1;
 #pragma unroll 1
-      for (int ti = 0; ti < n_tiles; ++ti) {
-        fetch(2, ti + 2);
+      for (int ti = 0; todo > 0; ++ti, --todo) {
+        fetch(2);
         uint32_t row = kNoRow;
         if (at[0] >= 0) {
           if (pg[0] >= 0 && pg[0] < P.n_pages) row = ((uint32_t)pg[0] << P.row_shift) + (uint32_t)at[0];
@@ -391,13 +394,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         for (uint32_t it = 0;; ++it) {
           const Item x = item_of(A, c);
           if ((x.flags & 3) == 1)
-            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.x.t1 - c.tile), total, ctas);
+            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
           wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
           ctl->item[it % kItems] = x;
           arrive(&ctl->item_full[it % kItems]);
-          c.tile += x.n_tiles - 1;
-          c.left -= x.n_tiles - 1;
-          if (!c.next(A, cls)) break;
+          if ((x.flags & 4) || !c.next(A, cls)) break;
         }
       }
       __syncwarp();
@@ -492,14 +493,16 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         const uint32_t p_lo = desc_lo(sb + C::kOffP, 128);
         uint32_t qslot = 0, qphase = 0, qit = 0, vslot = 1, vphase = 0, vit = 0, obuf = 0;
         int qleft = 0, vleft = 0, qn = 0, vn = 0;
+        int qlast = 0, vlast = 0;  // the item is the run's last
         bool first = true;
 #pragma unroll 1
-        for (int step = 0; step <= n_tiles; ++step) {
-          if (step < n_tiles) {  // scores of tile `step`
+        for (int step = 0;; ++step) {
+          if (qleft > 0 || !qlast) {  // scores of tile `step`
             const int ti = step;
             if (qleft == 0) {
               const Item& x = item_at(qit);
               qleft = x.n_tiles;
+              qlast = x.flags & 4;
               qn = (x.R + 15) / 16;
               wait(&ctl->q_full[qit & 1], (qit >> 1) & 1);
             }
@@ -532,6 +535,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             if (vleft == 0) {
               const Item& x = item_at(vit++);
               vleft = x.n_tiles;
+              vlast = x.flags & 4;
               vn = F8 ? (x.R + 15) / 16 * 6 : (x.R + 7) / 8 * 2;
               first = true;
               obuf = (vit - 1) % C::kOBufs;
@@ -562,6 +566,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               vslot -= S;
               vphase ^= 1;
             }
+            if (vleft == 0 && vlast) break;
           }
         }
         if (elect_one()) mma_commit(&ctl->fin);  // every product and arrival is done before the block ends
