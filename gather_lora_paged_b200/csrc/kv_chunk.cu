@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       bar_init(&ctl->p_full[lane][1], 128);
       bar_init(&ctl->o_full[lane], 1);
     }
+    if (lane < kItems) ctl->item[lane].flags = 4;  // what those see who did not wait for an entry (see wait_slow)
     if (lane == 0) {
       bar_init(&ctl->q_full, 256);
       bar_init(&ctl->q_empty, 1);
@@ -168,6 +169,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   }
   __syncthreads();  // the barriers are there
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
+  // Nobody walks on through items that may never come once a wait has given up.
+  auto over = [&]() -> bool { return *reinterpret_cast<volatile int*>(&ctl->dead); };
   // An item's entry.  It is written again for item it + 4, once both softmax groups are through with
   // this one; all others have read it by then.
   auto item_at = [&](uint32_t it) -> const Item& {
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           }
           __syncwarp();
         }
-        if (last) break;
+        if (last || __any_sync(FULL_MASK, over())) break;
       }
       if (elect_one()) mma_commit(&ctl->fin);  // every product and arrival is done before the block ends
       __syncwarp();
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           have = have_next;
         }
       }
-      if (last) break;
+      if (last || __any_sync(FULL_MASK, over())) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
@@ -668,10 +671,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         ti += n_tiles;
       }
       // all four warps are through with the entry
-      if (wg == 0) asm volatile("barrier.sync 1, 128;" ::: "memory");
-      else asm volatile("barrier.sync 2, 128;" ::: "memory");
+      const bool stop = wg == 0 ? any_of<1, 128>(over()) : any_of<2, 128>(over());
       if ((tid & 127) == 0) arrive(&ctl->item_empty[it % kItems]);
-      if (flags & 4) break;
+      if (stop || (flags & 4)) break;
     }
   }
   tc_fence_before();

@@ -162,16 +162,6 @@ __device__ __forceinline__ void wait_ld_n(float* v) {
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // The softmax warps' and the epilogue warps' barriers, and votes over them.
-template <int ID, int N>
-__device__ __forceinline__ void sync_of() { asm volatile("barrier.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
-template <int ID, int N>
-__device__ __forceinline__ bool any_of(bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.red.or.pred b, %2, %3, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r) : "r"((uint32_t)p), "n"(ID), "n"(N) : "memory");
-  return r;
-}
 __device__ __forceinline__ void softmax_sync() { sync_of<1, 256>(); }
 __device__ __forceinline__ bool softmax_any(bool p) { return any_of<2, 256>(p); }
 __device__ __forceinline__ void epilogue_sync() { sync_of<3, 128>(); }
@@ -252,6 +242,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       bar_init(&ctl->item_empty[lane], 1);
       bar_init(&ctl->rows_full[lane], 64);
     }
+    if (lane < kItems) ctl->item[lane].flags = 4;  // what those see who did not wait for an entry (see wait_slow)
     if (lane == 0) {
       bar_init(&ctl->tmem_full, 32);
       bar_init(&ctl->fin, 1);
@@ -259,7 +250,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  constexpr int E = TM <= 16 ? 1 : 2;  // an item's lead: measured 0.5 to 1.5 tiles
+  // an item's lead.  0, 1, 2 tiles: 256 tokens (8 rows, 16-bit) 500, 488, 501 us, 64 tokens over an e4m3 cache 138,
+  // 130, 128; 2, 4 tiles: a mixed step with items of 40 rows 145, 142.
+  constexpr int E = TM <= 16 ? 1 : 3;
   Cursor<TM, kTK, E> c;
   long long total, u1;
   int ctas;
@@ -270,6 +263,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 
   __syncthreads();  // the barriers are there
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
+  // Nobody walks on through items that may never come once a wait has given up.
+  auto over = [&]() -> bool { return *reinterpret_cast<volatile int*>(&ctl->dead); };
   auto tmem_at = [&]() -> uint32_t {  // for those who do not allocate it
     wait(&ctl->tmem_full, 0);
     return ctl->tmem;
@@ -315,6 +310,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             const Item& x = item_at(it++);
             left = x.n_tiles;
             last = x.flags & 4;
+            if (__any_sync(FULL_MASK, over())) left = last = 1;
             j = x.tile * kTK + key;
             lo = x.lo;
             hi = x.hi;
@@ -474,7 +470,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         arrive_copies(&ctl->q_full[it & 1]);
         arrive(&ctl->q_full[it & 1]);
         arrive(&ctl->rows_full[it % kItems]);
-        if (last) break;
+        if (last || __any_sync(FULL_MASK, over())) break;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 12) {
@@ -503,6 +499,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               const Item& x = item_at(qit);
               qleft = x.n_tiles;
               qlast = x.flags & 4;
+              if (__any_sync(FULL_MASK, over())) break;
               qn = (x.R + 15) / 16;
               wait(&ctl->q_full[qit & 1], (qit >> 1) & 1);
             }
@@ -536,6 +533,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               const Item& x = item_at(vit++);
               vleft = x.n_tiles;
               vlast = x.flags & 4;
+              if (__any_sync(FULL_MASK, over())) break;
               vn = F8 ? (x.R + 15) / 16 * 6 : (x.R + 7) / 8 * 2;
               first = true;
               obuf = (vit - 1) % C::kOBufs;
@@ -619,7 +617,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       auto muls = [&](int u, int i) -> uint64_t {
         return kRegs ? pair(qm[kRegs ? i : 0], qm[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(qmul + row_of(u) + i);
       };
-      softmax_sync();
+      if (softmax_any(over())) break;
 #pragma unroll 1
       for (int n = 0; n < n_here; ++n, ++ti) {
         const uint32_t sbuf = ts + (ti & 1) * C::kSCols;
@@ -860,7 +858,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       const float unit = ctl->unit[it & 1];
-      epilogue_sync();
+      if (epilogue_any(over())) break;
       wait(&ctl->o_full[it % C::kOBufs], (it / C::kOBufs) & 1);
       tc_fence_after();
       uint32_t bad[2] = {0, 0};

@@ -67,6 +67,17 @@ __device__ __forceinline__ float warp_max(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
+// A barrier of N threads, and a vote over it.
+template <int ID, int N>
+__device__ __forceinline__ void sync_of() { asm volatile("barrier.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
+template <int ID, int N>
+__device__ __forceinline__ bool any_of(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.red.or.pred b, %2, %3, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r) : "r"((uint32_t)p), "n"(ID), "n"(N) : "memory");
+  return r;
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -105,7 +116,8 @@ __device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swi
   return sbo >> 4 | 1u << 14 | swizzle << 29;
 }
 constexpr uint32_t kNoSwizzle = 0, kSwizzle128 = 2, kSwizzle64 = 4;
-// The slow part of a wait: bounded, and over at once when another one gave up.
+// The slow part of a wait: bounded, and over at once when another one gave up; nobody waits any more
+// then, and all roles come to their ends over what shared memory holds.
 __device__ __forceinline__ void wait_slow(uint64_t* b, uint32_t parity, int* dead, int32_t* err) {
   const long long t0 = clock64();
   for (;;) {

@@ -1320,9 +1320,7 @@ slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout
   A.lse = lse;
   A.Hq = n_q_heads;
   A.G = n_q_heads / layout->n_kv_heads;
-  if ((int64_t)A.G * std::min(max_rows, T) > (1ll << 30))
-    return P->fail(SLORA_ERR_UNSUPPORTED, "a sequence of 2^30 rows per kv head or more");
-  divide_by(A.G, A.g_mul, A.g_shift);
+  divide_by(A.G, A.g_mul, A.g_shift);  // rows: at most 2^20 tokens of 2^10 heads
   A.c = (float)((double)scale * 1.4426950408889634);
   A.window = window;
   A.max_rows = std::min(max_rows, T);

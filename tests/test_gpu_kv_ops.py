@@ -282,6 +282,43 @@ def test_quotients_next_to_a_border_take_the_exact_code():
     assert np.array_equal(got, want), np.argwhere(got != want)[:5]
 
 
+def _quantised(rows, dtype):
+    """Writes (n, 128) values as one head's K rows; the codes and scales in the pages."""
+    n = len(rows)
+    c = Cache([(n, n)], 1, 128, dtype, 1, 32768)
+    bits = R.to_bits(rows, dtype)
+    k = _dev(rows, dtype)
+    G.slora_kv_write(c.pool.h, c.layout, k, 128, k, 128, *c.batch())
+    assert c.check()[0] == 0
+    codes, scales = c.raw()
+    pos = np.arange(n)
+    pg, sl = c.table[0, pos // c.pt], pos % c.pt
+    return R.from_bits(bits, dtype), codes[pg, 1, 0, sl], scales[pg, 1, 0, sl]
+
+
+@pytest.mark.parametrize("shift", [-20, -138, 90])
+def test_every_pair_of_bf16_significands(shift):
+    """Each largest significand with every other one, 0 to 17 binades below it: ties where 7 divides either."""
+    sig = np.arange(128.0, 256.0)
+    rows = np.array([np.minimum(np.append(a * 2.0 ** (e + 1), sig[:127]), a * 2.0 ** (e + 1)) for e in range(18) for a in sig])
+    x, codes, scales = _quantised(rows * 2.0 ** shift, "bf16")
+    want, sw = R.quantise(x)
+    assert np.array_equal(scales, sw) and np.array_equal(codes, want), np.argwhere(codes != want)[:5]
+
+
+@pytest.mark.parametrize("shift", [-12, -24, 4])
+def test_every_largest_fp16_significand(shift):
+    """... with values at and around its borders, and random ones."""
+    rng = np.random.default_rng(shift + 100)
+    top = np.arange(1024.0, 2048.0).repeat(4)[:, None]
+    grid = R.e4m3_values()[:127]
+    border = ((grid[1:] + grid[:-1]) / 2)[rng.integers(0, 126, (len(top), 64))] * top / 448
+    rows = np.concatenate([top, border, rng.uniform(0, 1, (len(top), 63)) * top], 1) * rng.choice([-1, 1], (len(top), 128))
+    x, codes, scales = _quantised(rows * 2.0 ** shift, "f16")
+    want, sw = R.quantise(x)
+    assert np.array_equal(scales, sw) and np.array_equal(codes, want), np.argwhere(codes != want)[:5]
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_rows_that_are_not_finite_or_tiny(dtype):
     torch = _torch()
@@ -404,6 +441,73 @@ def test_attention(lens, H, group, D, dtype, fmt, pe, window):
     # the same bits again, and without lse
     again, lse2 = _attend(c, q, hq, window=window)
     assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("n,group,D,fmt,B", [(1, 1, 128, 0, 100), (1, 8, 128, 1, 100), (1, 8, 64, 0, 100), (2, 8, 64, 1, 100),
+                                             (4, 8, 128, 0, 80), (5, 8, 64, 1, 80), (5, 8, 128, 1, 60), (9, 8, 128, 0, 50),
+                                             (9, 8, 64, 1, 50)])
+def test_attention_many_short_items_per_cta(n, group, D, fmt, B):
+    """Several items of one to three key tiles in each CTA's run, so that all roles are items apart."""
+    rng = np.random.default_rng(n * group + D)
+    lens = [(n, n + int(np.exp(rng.uniform(0, np.log(330))))) for _ in range(B)]
+    H = 6
+    c = Cache(lens, H, D, "f16", fmt, 16384)
+    c.fill()
+    qv, q = _q(c, H * group)
+    out, lse = _attend(c, q, H * group)
+    assert c.check()[0] == 0
+    _compare(c, qv, out, lse, H * group, once=n * group > 32)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("rows", [4, 5, 7, 8, 9, 15, 16, 17, 31, 32, 33, 47, 48, 49])
+def test_attention_at_the_borders_of_row_tiles(rows, fmt):
+    for n, group in {(1, rows), (rows, 1)}:
+        c = Cache([(n, 300), (1, 70)], 2, 64, "bf16", fmt, 4096)
+        c.fill()
+        qv, q = _q(c, 2 * group)
+        out, lse = _attend(c, q, 2 * group)
+        assert c.check()[0] == 0
+        _compare(c, qv, out, lse, 2 * group, once=rows > 32)
+
+
+@pytest.mark.parametrize("n,group,D,fmt", [(1, 2, 64, 0), (3, 2, 128, 1), (40, 2, 64, 0)])
+def test_attention_one_item_over_every_cta(n, group, D, fmt):
+    """A partial from each CTA: more of them than a warp has lanes."""
+    c = Cache([(n, 40000)], 1, D, "bf16", fmt, 65536)
+    c.fill()
+    qv, q = _q(c, group)
+    out, lse = _attend(c, q, group)
+    assert c.check()[0] == 0
+    _compare(c, qv, out, lse, group, once=n * group > 32)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("group", [2, 20])
+def test_rows_that_see_nothing_beside_infinities(group, fmt):
+    """Rows before the first token get 0 and -inf whatever the item's V rows hold."""
+    def spoil(b, part, x):
+        if part:
+            x[0, :, 3], x[1, 0, 7] = np.inf, np.nan
+    c = Cache([(6, 4), (2, 300)], 2, 64, "bf16", fmt, 4096)
+    c.fill(spoil=spoil)
+    qv, q = _q(c, 2 * group)
+    out, lse = _attend(c, q, 2 * group)
+    assert bool((out[:2] == 0).all()) and bool((lse[:2] == -math.inf).all())
+    _compare(c, qv, out, lse, 2 * group, once=True)
+
+
+@pytest.mark.parametrize("group,n", [(1, 1), (8, 2), (8, 40)])
+def test_attention_where_every_sequence_fits_one_tile(group, n):
+    """A table of at most 128 positions, at 128 and below: nothing is joined."""
+    for longest in (128, 127):
+        c = Cache([(n, longest), (1, 1), (n, n)], 2, 128, "f16", 0, 512)
+        assert c.pt == 1 or c.ldb * c.pt >= longest
+        c.fill()
+        qv, q = _q(c, 2 * group)
+        out, lse = _attend(c, q, 2 * group)
+        assert c.check()[0] == 0
+        _compare(c, qv, out, lse, 2 * group, once=n * group > 32)
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
