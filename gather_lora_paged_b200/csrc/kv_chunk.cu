@@ -37,6 +37,7 @@ namespace {
 constexpr int kNT = 512;
 constexpr int kTM = 256;      // rows per item
 constexpr int kTK = kKvTile;  // keys per tile
+constexpr int kHalf = kTK / 2;
 constexpr int kMinRun = 2;
 constexpr int kLead = 2;      // an item's lead: q and the outputs cost about two tiles
 constexpr int kItems = 4;     // items that are known ahead
@@ -45,6 +46,10 @@ constexpr float kSlack = 8.f; // log2 of the largest weight
 
 template <int FMT, int D>
 struct Cfg {
+  // Keys of one S, the softmax's step.  With 64, S of the next tile's half is computed while the softmax is at
+  // the other half, but an MMA of N = 64 takes 55 cycles, of N = 128 69: 16-bit chunks over 8192 take 1249 us
+  // with 64 and 1145 with 128; in e4m3, where the softmax has more to do, a mixed step takes 122 and 145.
+  static constexpr int kPart = FMT == SLORA_KV_16 ? 128 : 64;
   static constexpr int kPanel = 128 * 128;                 // 128 rows of 64 16-bit elements
   static constexpr int kSlot = D / 64 * kPanel;            // K or V of a tile
   static constexpr int kSlots = FMT == SLORA_KV_16 ? 5 : 4;
@@ -59,7 +64,7 @@ struct Cfg {
 template <int S>
 struct Ctl {
   uint64_t kv_full[S], kv_empty[S], q_full, q_empty, item_full[kItems], item_empty[kItems], rows_full[kItems];
-  uint64_t s_full[2], p_full[2][2], o_full[2], tmem_full, fin;  // p_full[q tile][half of the keys]
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], tmem_full, fin;  // [q tile][part, half of the keys]
   Item item[kItems];
   uint32_t tmem;
   int dead;                    // a wait gave up: nobody waits any more
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   using C = Cfg<FMT, D>;
   constexpr bool F8 = FMT == SLORA_KV_E4M3;
   constexpr int MT = F8 ? SLORA_F16 : DT;  // operand type of the products
-  constexpr int S = C::kSlots;
+  constexpr int S = C::kSlots, kPart = C::kPart, kParts = kTK / kPart;
   using Control = Ctl<S>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
@@ -145,7 +150,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       bar_init(&ctl->rows_full[lane], 128);
     }
     if (lane < 2) {
-      bar_init(&ctl->s_full[lane], 1);
+      bar_init(&ctl->s_full[lane][0], 1);
+      bar_init(&ctl->s_full[lane][1], 1);
+      bar_init(&ctl->pv_done[lane], 1);
       bar_init(&ctl->p_full[lane][0], 128);
       bar_init(&ctl->p_full[lane][1], 128);
       bar_init(&ctl->o_full[lane], 1);
@@ -204,38 +211,40 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       arrive(&ctl->tmem_full);
       const uint32_t fmt = MT == SLORA_BF16 ? 1u : 0u;
       const uint32_t id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
-      const uint32_t id_s = id0 | ((uint32_t)kTK >> 3) << 17, id_o = id0 | (1u << 16) | ((uint32_t)D >> 3) << 17;  // V: MN-major
+      const uint32_t id_s = id0 | ((uint32_t)kPart >> 3) << 17, id_o = id0 | (1u << 16) | ((uint32_t)D >> 3) << 17;  // V: MN-major
       const uint32_t hi = desc_hi(1024, kSwizzle128);
       const uint32_t q_lo = desc_lo(sb, 16), k_lo = desc_lo(sb + C::kOffRing, 16), v_lo = desc_lo(sb + C::kOffRing, C::kPanel);
-      uint32_t g = 0, pn = 0;  // slots so far, tiles so far
-      uint32_t pn1 = 0;        // of the second q tile
-      auto qk = [&](int i, uint32_t slot) {
-        const uint32_t a = q_lo + i * (C::kSlot >> 4), b = k_lo + slot * (C::kSlot >> 4);
+      uint32_t g = 0, parity = 0;  // slots so far; a bit per q tile, of its weights' barriers
+      auto qk = [&](int i, int part, uint32_t slot) {
+        const uint32_t a = q_lo + i * (C::kSlot >> 4), b = k_lo + slot * (C::kSlot >> 4) + part * ((kPart * 128) >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * C::kPanel + (k & 3) * 32) >> 4;
-          mma<false>(tmem + i * 128, a + off, hi, b + off, hi, id_s, k > 0);
+          mma<false>(tmem + i * 128 + part * kPart, a + off, hi, b + off, hi, id_s, k > 0);
         }
-        mma_commit(&ctl->s_full[i]);
+        mma_commit(&ctl->s_full[i][part]);
       };
       auto pv = [&](int i, int half, uint32_t slot, bool first) {
-        const uint32_t b = v_lo + slot * (C::kSlot >> 4) + half * ((kTK / 32 * 2048) >> 4), a = tmem + i * 128 + half * 32;
+        const uint32_t b = v_lo + slot * (C::kSlot >> 4) + half * ((kHalf * 128) >> 4), a = tmem + i * 128 + half * (kPart == 128 ? 32 : 64);
 #pragma unroll
-        for (int k = 0; k < kTK / 32; ++k)
+        for (int k = 0; k < kHalf / 16; ++k)
           mma_ts(tmem + 256 + i * 128, a + k * 8, b + ((k * 2048) >> 4), hi, id_o, !(first && half == 0 && k == 0));
+        mma_commit(&ctl->pv_done[i]);
       };
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
         const Item& x = item_at(it);
-        const int n_tiles = x.n_tiles, last = x.flags & 4;
-        const bool two = x.R > 128;
+        const int n_tiles = x.n_tiles, last = x.flags & 4, q_tiles = x.R > 128 ? 2 : 1;
         wait(&ctl->q_full, it & 1);
         wait(&ctl->kv_full[g % S], (g / S) & 1);
         fence_async_smem();
         tc_fence_after();
         if (elect_one()) {
-          qk(0, g % S);
-          if (two) qk(1, g % S);
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+            qk(0, part, g % S);
+            if (q_tiles == 2) qk(1, part, g % S);
+          }
           mma_commit(&ctl->kv_empty[g % S]);
           if (n_tiles == 1) mma_commit(&ctl->q_empty);
         }
@@ -245,46 +254,26 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           const bool more = n + 1 < n_tiles;
           const uint32_t v = (g + 1) % S, k = (g + 2) % S;
           wait(&ctl->kv_full[v], ((g + 1) / S) & 1);
-          wait(&ctl->p_full[0][0], pn & 1);
-          fence_async_smem();
-          tc_fence_after();
-          if (elect_one()) pv(0, 0, v, n == 0);
-          __syncwarp();
-          wait(&ctl->p_full[0][1], pn++ & 1);
-          tc_fence_after();
-          if (elect_one()) {
-            pv(0, 1, v, n == 0);
-            if (!more) mma_commit(&ctl->o_full[0]);
-          }
-          __syncwarp();
-          if (more) {
-            wait(&ctl->kv_full[k], ((g + 2) / S) & 1);
+          if (more) wait(&ctl->kv_full[k], ((g + 2) / S) & 1);
+#pragma unroll 1
+          for (int step = 0; step < 2 * q_tiles; ++step) {  // in the order in which the weights come
+            const int i = kParts == 1 ? step >> 1 : step & (q_tiles - 1), half = kParts == 1 ? step & 1 : step >> (q_tiles - 1);
+            wait(&ctl->p_full[i][half], (parity >> i) & 1);
             fence_async_smem();
             tc_fence_after();
-            if (elect_one()) qk(0, k);
+            if (elect_one()) {
+              pv(i, half, v, n == 0);
+              if (half == 1 && !more) mma_commit(&ctl->o_full[i]);
+              if (more && (kParts == 2 || half == 1)) qk(i, kParts == 2 ? half : 0, k);
+              if (step + 1 == 2 * q_tiles) {
+                mma_commit(&ctl->kv_empty[v]);
+                if (more) mma_commit(&ctl->kv_empty[k]);
+                if (n + 2 == n_tiles) mma_commit(&ctl->q_empty);
+              }
+            }
             __syncwarp();
           }
-          if (two) {
-            wait(&ctl->p_full[1][0], pn1 & 1);
-            tc_fence_after();
-            if (elect_one()) pv(1, 0, v, n == 0);
-            __syncwarp();
-            wait(&ctl->p_full[1][1], pn1++ & 1);
-            tc_fence_after();
-          }
-          if (elect_one()) {
-            if (two) {
-              pv(1, 1, v, n == 0);
-              if (!more) mma_commit(&ctl->o_full[1]);
-            }
-            mma_commit(&ctl->kv_empty[v]);
-            if (more) {
-              if (two) qk(1, k);
-              mma_commit(&ctl->kv_empty[k]);
-              if (n + 2 == n_tiles) mma_commit(&ctl->q_empty);
-            }
-          }
-          __syncwarp();
+          parity ^= 3u >> (2 - q_tiles);
         }
         if (last || __any_sync(FULL_MASK, over())) break;
       }
@@ -460,8 +449,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
     wait(&ctl->tmem_full, 0);
     const uint32_t tmem = ctl->tmem;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + wg * 128, to = tmem + lanes + 256 + wg * 128;
-    uint32_t sn = 0, on = 0, ti = 0;
+    const uint32_t tq = tmem + lanes + wg * 128, to = tmem + lanes + 256 + wg * 128;
+    uint32_t sn = 0, on = 0, ti = 0, pv = 0;  // tiles with this q tile, items with it, tiles; weights handed over
 #pragma unroll 1
     for (uint32_t it = 0;; ++it) {
       const Item& x = item_at(it);
@@ -479,60 +468,15 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           cr = qscale[(it % kItems) * kTM + r];
         }
 #pragma unroll 1
-        for (int n = 0; n < n_tiles; ++n, ++ti) {
+        for (int n = 0; n < n_tiles; ++n, ++ti, ++sn) {
           const uint32_t g = 2 * ti + 1;
-          // scales and mask, scores
-          wait_for_both(&ctl->kv_full[g % S], (g / S) & 1, &ctl->s_full[wg], sn++ & 1, &ctl->dead, P.err);
-          tc_fence_after();
-          float s[kTK];
-          ld32(ts, s);
-          ld32(ts + 32, s + 32);
+          wait(&ctl->kv_full[g % S], (g / S) & 1);  // scales and mask
           const float* const ks = scales + (ti % kMeta) * 2 * kTK;
           const int key0 = (tile0 + n) * kTK;
           const uint4 have = *reinterpret_cast<const uint4*>(ctl->mask[ti % kMeta]);
           const bool masked = key0 + kTK - 1 > pmin || (A.window > 0 && key0 <= pmax - A.window) ||
                               (have.x & have.y & have.z & have.w) != FULL_MASK;
-          const uint32_t hv[4] = {have.x, have.y, have.z, have.w};
-          float top[2] = {-INFINITY, -INFINITY};
-          // scales, masks and maxima of 32 scores
-          auto take = [&](int w) {
-            float* const x = s + w * 32;
-            if (F8) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(ks + w * 32 + i);
-                unpair(mul2(pair(x[i], x[i + 1]), k4.x), x[i], x[i + 1]);
-                unpair(mul2(pair(x[i + 2], x[i + 3]), k4.y), x[i + 2], x[i + 3]);
-              }
-            }
-            if (masked) {  // bits of the keys lo < i <= hi
-              const int hi = pos - key0 - 32 * w + 1, lo = low - key0 - 32 * w + 1;
-              const int h2 = min(max(hi, 0), 32), l2 = min(max(lo, 0), 32);
-              const uint32_t below_h = h2 == 32 ? FULL_MASK : (1u << h2) - 1, below_l = l2 == 32 ? FULL_MASK : (1u << l2) - 1;
-              const uint32_t seen = hv[w] & below_h & ~below_l;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((seen >> i) & 1)) x[i] = -INFINITY;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              top[0] = max3(top[0], x[i], x[i + 1]);
-              top[1] = max3(top[1], x[i + 2], x[i + 3]);
-            }
-          };
-          wait_ld32(s);
-          wait_ld32(s + 32);
-          take(0);
-          take(1);
-          ld32(ts + 64, s + 64);
-          ld32(ts + 96, s + 96);
-          wait_ld32(s + 64);
-          wait_ld32(s + 96);
-          take(2);
-          take(3);
-          const float mn = fmaxf(m, fmaxf(top[0], top[1]) * cr);
           float ratio = 1.f;
-          bool raise = false;
           if (F8) {
             const float4 v4 = *reinterpret_cast<const float4*>(ks + kTK + lane * 4);
             const float tv = warp_max(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)));
@@ -540,67 +484,111 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
               const float v = fmaxf(2.f * tv, 0x1p-126f);
               ratio = vn / v;
               vn = v;
-              raise = true;
             }
           }
-          if (__any_sync(FULL_MASK, mn > m + kSlack) || raise) {
-            const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
-            m = mn;
-            l *= a;
-            if (n > 0) {
-              const float f = a * ratio;
 #pragma unroll 1
-              for (int i = 0; i < D; i += 32) {
-                float o[32];
-                ld32(to + i, o);
-                wait_ld32(o);
+          for (int part = 0; part < kParts; ++part) {
+            const uint32_t ts = tq + part * kPart;
+            wait(&ctl->s_full[wg][part], sn & 1);
+            tc_fence_after();
+            float s[kPart];
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const float* const kh = ks + part * kPart;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= f;
-                st32(to + i, o);
-              }
-            }
-          }
-          const float mz = m == -INFINITY ? 0.f : m;
-          const float vinv = F8 ? __frcp_rn(vn) : 1.f;
-          const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz), vi2 = pair(vinv, vinv);
-          uint64_t ls[2] = {0, 0};
-          auto weigh = [&](auto all_seen) {  // the weights, from the scores
-            constexpr bool kOpen = decltype(all_seen)::value;
+            for (int h = 0; h < kPart; h += 64) {
+              ld32(ts + h, s + h);
+              ld32(ts + h + 32, s + h + 32);
+              wait_ld32(s + h);
+              wait_ld32(s + h + 32);
+              if (F8) {
 #pragma unroll
-            for (int i = 0; i < kTK; i += 32) {
-              uint32_t w[16];
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                float p[2];
-                unpair(fma2(pair(s[i + k], s[i + k + 1]), c2, m2), p[0], p[1]);
-                p[0] = ex2(p[0]);
-                p[1] = ex2(p[1]);
-                uint64_t pp = pair(p[0], p[1]);
-                ls[(k >> 1) & 1] = add2(ls[(k >> 1) & 1], pp);
-                if (F8) {
-                  pp = mul2(pp, mul2(*reinterpret_cast<const uint64_t*>(ks + kTK + i + k), vi2));
-                  float q[2];
-                  unpair(pp, q[0], q[1]);
-                  if (!kOpen) {  // a NaN scale of an unseen key stays out
-                    q[0] = p[0] == 0.f ? 0.f : q[0];
-                    q[1] = p[1] == 0.f ? 0.f : q[1];
-                  }
-                  w[k / 2] = pk2<MT>(q[0], q[1]);
-                } else {
-                  w[k / 2] = pk2<MT>(p[0], p[1]);
+                for (int i = h; i < h + 64; i += 4) {
+                  const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(kh + i);
+                  unpair(mul2(pair(s[i], s[i + 1]), k4.x), s[i], s[i + 1]);
+                  unpair(mul2(pair(s[i + 2], s[i + 3]), k4.y), s[i + 2], s[i + 3]);
                 }
               }
-              st16(ts + i / 2, w);
-              if (i == 32 || i == 96) {  // the products with half of the keys may begin
-                wait_st();
-                tc_fence_before();
-                arrive(&ctl->p_full[wg][i / 64]);
+              if (masked) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {  // bits of the keys low < j <= pos
+                  const int word = (part * kPart + h) / 32 + w, base = key0 + 32 * word - 1;
+                  const int h2 = min(max(pos - base, 0), 32), l2 = min(max(low - base, 0), 32);
+                  const uint32_t below_h = h2 == 32 ? FULL_MASK : (1u << h2) - 1, below_l = l2 == 32 ? FULL_MASK : (1u << l2) - 1;
+                  const uint32_t there = ctl->mask[ti % kMeta][word];
+                  const uint32_t seen = there & below_h & ~below_l;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (!((seen >> i) & 1)) s[h + w * 32 + i] = -INFINITY;
+                }
+              }
+#pragma unroll
+              for (int i = h; i < h + 64; i += 8) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) top[q] = max3(top[q], s[i + 2 * q], s[i + 2 * q + 1]);
               }
             }
-          };
-          if (masked) weigh(std::false_type{});
-          else weigh(std::true_type{});
-          {
+            const float mn = fmaxf(m, fmaxf(max3(top[0], top[1], top[2]), top[3]) * cr);
+            if (__any_sync(FULL_MASK, mn > m + kSlack) || (F8 && ratio != 1.f)) {
+              const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
+              m = mn;
+              l *= a;
+              if (n > 0 || part > 0) {
+                wait(&ctl->pv_done[wg], (pv + 1) & 1);  // the products so far
+                tc_fence_after();
+                const float f = a * ratio;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                  float o[32];
+                  ld32(to + i, o);
+                  wait_ld32(o);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) o[k] *= f;
+                  st32(to + i, o);
+                }
+              }
+              ratio = 1.f;
+            }
+            const float mz = m == -INFINITY ? 0.f : m;
+            const float vinv = F8 ? __frcp_rn(vn) : 1.f;
+            const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz), vi2 = pair(vinv, vinv);
+            uint64_t ls[2] = {0, 0};
+            auto weigh = [&](auto all_seen) {  // the weights, from the scores
+              constexpr bool kOpen = decltype(all_seen)::value;
+#pragma unroll
+              for (int i = 0; i < kPart; i += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                  float p[2];
+                  unpair(fma2(pair(s[i + k], s[i + k + 1]), c2, m2), p[0], p[1]);
+                  p[0] = ex2(p[0]);
+                  p[1] = ex2(p[1]);
+                  uint64_t pp = pair(p[0], p[1]);
+                  ls[(k >> 1) & 1] = add2(ls[(k >> 1) & 1], pp);
+                  if (F8) {
+                    pp = mul2(pp, mul2(*reinterpret_cast<const uint64_t*>(kh + kTK + i + k), vi2));
+                    float q[2];
+                    unpair(pp, q[0], q[1]);
+                    if (!kOpen) {  // a NaN scale of an unseen key stays out
+                      q[0] = p[0] == 0.f ? 0.f : q[0];
+                      q[1] = p[1] == 0.f ? 0.f : q[1];
+                    }
+                    w[k / 2] = pk2<MT>(q[0], q[1]);
+                  } else {
+                    w[k / 2] = pk2<MT>(p[0], p[1]);
+                  }
+                }
+                st16(ts + i / 2, w);
+                if (i % 64 == 32) {  // the products with these 64 keys may begin
+                  wait_st();
+                  tc_fence_before();
+                  arrive(&ctl->p_full[wg][part + i / 64]);
+                }
+              }
+            };
+            if (F8 && masked) weigh(std::false_type{});
+            else weigh(std::true_type{});
+            pv += kPart / 64;
             float a, b;
             unpair(add2(ls[0], ls[1]), a, b);
             l += a + b;
