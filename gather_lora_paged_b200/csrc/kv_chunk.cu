@@ -2,18 +2,20 @@
 // the KV pages on the 5th-generation tensor cores.  Definition and row order as
 // in kv_decode.cu; runs, partials and their join as in kv_attn.cuh.
 //
-// One CTA per SM, 12 warps; an item is 256 rows (token, head of the group) of
+// One CTA per SM, 16 warps; an item is 256 rows (token, head of the group) of
 // one kv head as two M = 128 tiles, its keys come 128 at a time:
-//   warps 8..10  copy q once per item and K, V of each tile from the pages into a
-//                ring of shared-memory slots (128-byte swizzle, K K-major, V as the
-//                MN-major operand of P.V; a page may hold one token, so rows are
-//                gathered by 16-byte cp.async).  e4m3 codes become their exact fp16
-//                values on the way.
-//   warp 11      one thread issues, per tile n and q tile i, P_i.V_n and S_i =
-//                Q_i.K_(n+1)^T (tcgen05.mma, P_i from TMEM), so that the softmax of
-//                one q tile runs while the tensor cores work for the other.
-//   warps 0..3, 4..7   the softmax of q tile 0 and 1: a thread owns a row, reads its 128
-//                scores from TMEM, and writes the weights back over them in 16 bits.
+//   warps 8..11 copy q once per item and K, V of each tile from the pages into a
+//               ring of shared-memory slots (128-byte swizzle, K K-major, V as the
+//               MN-major operand of P.V; a page may hold one token, so rows are
+//               gathered by 16-byte cp.async, whose arrivals fill a slot's barrier).
+//               e4m3 codes become their exact fp16 values on the way.
+//   warp 12     issues, per q tile i, P_i.V_n as its weights come and S_i = Q_i.K_(n+1)^T behind
+//               them (tcgen05.mma, P_i from TMEM), so that the softmax of
+//               one q tile runs while the tensor cores work for the other.
+//   warp 13     the run's items, for all others.
+//   warps 0..3, 4..7   the softmax of q tile 0 and 1: a thread owns a row, reads its
+//               scores from TMEM, and writes the weights back over them in 16 bits; at the
+//               item's end it writes the row.
 // TMEM: S0, S1 (128 columns each, P over S), O0, O1 (D columns each).
 // The reference point of a row's weights (its maximum so far) moves only when the
 // maximum has grown by 2^8: weights then reach at most 2^8, far inside
@@ -22,8 +24,15 @@
 // rounded once to the operand type, which puts an error of the size of the output's own
 // rounding on it (the two halves of kv_decode.cu would double the P.V
 // product, which is half the work here).
-// e4m3: K's scale multiplies the score, V's the weight, relative to a V scale
-// that is raised when a tile's largest is 8 times it.
+// e4m3: K's scale multiplies the score, V's the weight, relative to twice the largest
+// V scale met so far.
+//
+// What bounds it: both products of a tile take 2100 cycles (128 columns and 16 elements 64), the
+// exponentials of its 256 x 128 weights as long on the special-function units; a tile takes 3300, as
+// a q tile's softmax (2200) and its products (1050) follow one another.  2 x 1024..2048 tokens over 8192 keys, 64
+// heads on 8 of 128, bf16: 1.13 ms, 1040 TFLOP/s at 1.5 to 1.6 GHz (the power limit), tensor pipe 60 % of
+// the cycles.  A quarter of the exponentials as polynomials on the FMA pipe did not pay (1234 us for 1184):
+// the softmax waits for latencies and issue slots more than for the special-function units.
 #include <math.h>
 
 #include <type_traits>
@@ -37,7 +46,7 @@ namespace {
 constexpr int kNT = 512;
 constexpr int kTM = 256;      // rows per item
 constexpr int kTK = kKvTile;  // keys per tile
-constexpr int kHalf = kTK / 2;
+constexpr int kHalf = kTK / 2;  // weights are handed over for so many keys
 constexpr int kMinRun = 2;
 constexpr int kLead = 2;      // an item's lead: q and the outputs cost about two tiles
 constexpr int kItems = 4;     // items that are known ahead
