@@ -140,8 +140,9 @@ __device__ __forceinline__ long long share(long long a, int b, int c) {
   return a * b / c;
 }
 
-// This CTA's run of the line.  Every warp finds it by itself, a lane adding up some neighbouring
-// sequences: nobody waits for anybody.  Runs are at least E + min_tiles units, so that each has a tile.
+// This CTA's run of the line, found by one warp (some 400 instructions: 20 warps of a CTA that all
+// went through them spent 4500 cycles), a lane adding up some neighbouring
+// sequences.  Runs are at least E + min_tiles units, so that each has a tile.
 // False: this CTA has none.  total, ctas, u1: units in the line, runs, this run's end.
 template <int TM, int TK, int E>
 __device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_tiles, Cursor<TM, TK, E>& c,

@@ -166,7 +166,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       bar_init(&ctl->p_full[lane][1], 128);
       bar_init(&ctl->o_full[lane], 1);
     }
-    if (lane < kItems) ctl->item[lane].flags = 4;  // what those see who did not wait for an entry (see wait_slow)
+    if (lane < kItems) {  // what those see who did not wait for an entry (see wait_slow)
+      ctl->item[lane].flags = 4;
+      ctl->item[lane].n_tiles = 0;
+    }
     if (lane == 0) {
       bar_init(&ctl->q_full, 256);
       bar_init(&ctl->q_empty, 1);
@@ -175,13 +178,6 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       ctl->dead = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  Cursor<kTM, kTK, kLead> c;
-  long long total, u1;
-  int ctas;
-  if (!find_run<kTM, kTK, kLead>(A, cls, kMinRun, c, total, ctas, u1)) {
-    griddep_wait();
-    return;
   }
   __syncthreads();  // the barriers are there
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
@@ -200,15 +196,24 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 13) {
       // ------------------------------------------------------ the run's items
+      Cursor<kTM, kTK, kLead> c;
+      long long total, u1;
+      int ctas;
+      const bool any = find_run<kTM, kTK, kLead>(A, cls, kMinRun, c, total, ctas, u1);
       if (lane == 0) {
-        for (uint32_t it = 0;; ++it) {
-          const Item x = item_of(A, c);
-          if ((x.flags & 3) == 1)
-            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
-          wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
-          ctl->item[it % kItems] = x;
-          arrive(&ctl->item_full[it % kItems]);
-          if ((x.flags & 4) || !c.next(A, cls)) break;
+        if (!any) {
+          ctl->item[0].n_tiles = 0;
+          arrive(&ctl->item_full[0]);
+        } else {
+          for (uint32_t it = 0;; ++it) {
+            const Item x = item_of(A, c);
+            if ((x.flags & 3) == 1)
+              note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
+            wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
+            ctl->item[it % kItems] = x;
+            arrive(&ctl->item_full[it % kItems]);
+            if ((x.flags & 4) || !c.next(A, cls)) break;
+          }
         }
       }
       __syncwarp();
@@ -244,6 +249,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       for (uint32_t it = 0;; ++it) {
         const Item& x = item_at(it);
         const int n_tiles = x.n_tiles, last = x.flags & 4, q_tiles = x.R > 128 ? 2 : 1;
+        if (n_tiles == 0) break;
         wait(&ctl->q_full, it & 1);
         wait(&ctl->kv_full[g % S], (g / S) & 1);
         fence_async_smem();
@@ -303,6 +309,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
     for (uint32_t it = 0;; ++it) {
       const Item& x = item_at(it);
       const int n_tiles = x.n_tiles, lo = x.lo, hi = x.hi, b = x.b, off = x.h * P.pt, last = x.flags & 4;
+      if (n_tiles == 0) break;
       int j = x.tile * kTK + key;
       const int32_t* const table = P.blocks + (int64_t)b * P.ldb;
       int pg = 0, at = -1;                 // page and place in it (-1: no such key) of this lane's key in the next tile
@@ -464,6 +471,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
     for (uint32_t it = 0;; ++it) {
       const Item& x = item_at(it);
       const int n_tiles = x.n_tiles, tile0 = x.tile, R = x.R, flags = x.flags, first = x.first, r_item = x.rt * kTM;
+      const bool none = over() || n_tiles == 0;
+      if (wg == 0 ? any_of<1, 128>(none) : any_of<2, 128>(none)) break;
       if (wg == 0 || R > 128) {
         const int r = wg * 128 + (warp & 3) * 32 + lane;
         const int t = r < R ? token_of(A, r_item + r) : 0;
@@ -668,9 +677,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         ti += n_tiles;
       }
       // all four warps are through with the entry
-      const bool stop = wg == 0 ? any_of<1, 128>(over()) : any_of<2, 128>(over());
+      if (wg == 0) sync_of<1, 128>();
+      else sync_of<2, 128>();
       if ((tid & 127) == 0) arrive(&ctl->item_empty[it % kItems]);
-      if (stop || (flags & 4)) break;
+      if (flags & 4) break;
     }
   }
   tc_fence_before();

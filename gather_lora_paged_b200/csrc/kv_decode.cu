@@ -108,7 +108,8 @@ struct Ctl {
   alignas(16) float ref[TM];                  // the rows' references, negated
   float fac[TM];                              // what a move of them scales sums by
   // an item's end, for the epilogue: warps' sums, references, the weights' unit, and its own notes
-  float sum[2][4][TM], end_ref[2][TM], unit[2], out_fac[TM];
+  float sum[2][4][TM], end_ref[2][TM], unit[2];
+  alignas(8) float out_fac[TM];
   uint32_t bad[4][2];                         // warps' rows that are not finite
 };
 
@@ -248,7 +249,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       bar_init(&ctl->item_empty[lane], 1);
       bar_init(&ctl->rows_full[lane], 64);
     }
-    if (lane < kItems) ctl->item[lane].flags = 4;  // what those see who did not wait for an entry (see wait_slow)
+    if (lane < kItems) {  // what those see who did not wait for an entry (see wait_slow)
+      ctl->item[lane].flags = 4;
+      ctl->item[lane].n_tiles = 0;
+    }
     if (lane == 0) {
       bar_init(&ctl->tmem_full, 32);
       bar_init(&ctl->fin, 1);
@@ -256,17 +260,6 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // an item's lead.  0, 1, 2 tiles: 256 tokens (8 rows, 16-bit) 500, 488, 501 us, 64 tokens over an e4m3 cache 138,
-  // 130, 128; 2, 4 tiles: a mixed step with items of 40 rows 145, 142.
-  constexpr int E = TM <= 16 ? 1 : 3;
-  Cursor<TM, kTK, E> c;
-  long long total, u1;
-  int ctas;
-  if (!find_run<TM, kTK, E>(A, cls, kMinRun, c, total, ctas, u1)) {
-    if (blockIdx.x == 0) kv_record_bad(P, A.max_rows, tid, kNT);
-    return;
-  }
-
   __syncthreads();  // the barriers are there
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, &ctl->dead, P.err); };
   // Nobody walks on through items that may never come once a wait has given up.
@@ -301,22 +294,20 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       uint32_t swz[NSW];
 #pragma unroll
       for (int k = 0; k < NSW; ++k) swz[k] = place<W>(kTK, k * RPI + jl, cl) - k * RPI * W;
-      // the item whose tiles are looked up: the first one is known here
-      const Item x0 = item_of(A, c);
-      uint32_t it = 1;
-      int left = x0.n_tiles, j = x0.tile * kTK + key, lo = x0.lo, hi = x0.hi, b = x0.b, off = x0.h * P.pt, last = x0.flags & 4;
+      uint32_t it = 0;
+      int left = 0, j = 0, lo = 0, hi = 0, b = 0, off = 0, last = 0;  // the item whose tiles are looked up
       int todo = 0;  // tiles looked up and not yet copied
       int pg[3], at[3], sq[3];  // page and place in it (-1: no such key) of this lane's key, three tiles
       auto fetch = [&](int i) {
         at[i] = -1;
         pg[i] = 0;
         if (left > 0 || !last) {
-          ++todo;
           if (left == 0) {
             const Item& x = item_at(it++);
             left = x.n_tiles;
             last = x.flags & 4;
             if (__any_sync(FULL_MASK, over())) left = last = 1;
+            if (left == 0) return;  // no work for this CTA
             j = x.tile * kTK + key;
             lo = x.lo;
             hi = x.hi;
@@ -328,6 +319,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             pg[i] = __ldg(P.blocks + (int64_t)b * P.ldb + blk);
             at[i] = off + (j - blk * P.pt);
           }
+          ++todo;
           sq[i] = b;
           j += kTK;
           --left;
@@ -392,15 +384,27 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 13) {
       // ------------------------------------------------------ the run's items
+      // an item's lead.  0, 1, 2 tiles: 256 tokens (8 rows, 16-bit) 500, 488, 501 us, 64 tokens over an e4m3 cache 138,
+      // 130, 128; 2, 4 tiles: a mixed step with items of 40 rows 145, 142.
+      constexpr int E = TM <= 16 ? 1 : 3;
+      Cursor<TM, kTK, E> c;
+      long long total, u1;
+      int ctas;
+      const bool any = find_run<TM, kTK, E>(A, cls, kMinRun, c, total, ctas, u1);
       if (lane == 0) {
-        for (uint32_t it = 0;; ++it) {
-          const Item x = item_of(A, c);
-          if ((x.flags & 3) == 1)
-            note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
-          wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
-          ctl->item[it % kItems] = x;
-          arrive(&ctl->item_full[it % kItems]);
-          if ((x.flags & 4) || !c.next(A, cls)) break;
+        if (!any) {
+          ctl->item[0].n_tiles = 0;
+          arrive(&ctl->item_full[0]);
+        } else {
+          for (uint32_t it = 0;; ++it) {
+            const Item x = item_of(A, c);
+            if ((x.flags & 3) == 1)
+              note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
+            wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
+            ctl->item[it % kItems] = x;
+            arrive(&ctl->item_full[it % kItems]);
+            if ((x.flags & 4) || !c.next(A, cls)) break;
+          }
         }
       }
       __syncwarp();
@@ -410,6 +414,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
         const Item& x = item_at(it);
+        if (x.n_tiles == 0) break;
         const int R = x.R, r_item = x.rt * TM, row0 = x.row0, hq0 = x.h * A.G, last = x.flags & 4;
         const uint32_t dst = sb + C::kOffQ + (it & 1) * C::kQ;
         for (int r = lane + 32 * qw; r < C::kRows16; r += 64)
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               const Item& x = item_at(qit);
               qleft = x.n_tiles;
               qlast = x.flags & 4;
-              if (__any_sync(FULL_MASK, over())) break;
+              if (qleft == 0 || __any_sync(FULL_MASK, over())) break;
               qn = (x.R + 15) / 16;
               wait(&ctl->q_full[qit & 1], (qit >> 1) & 1);
             }
@@ -604,6 +609,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     for (uint32_t it = 0;; ++it) {
       const Item& x_ = item_at(it);
       const int n_here = x_.n_tiles, tile0 = x_.tile, R = x_.R, flags = x_.flags;
+      if (softmax_any(over() || n_here == 0)) break;
       const uint32_t to = ts + 2 * C::kSCols + it % C::kOBufs * C::kPCols;
       wait(&ctl->rows_full[it % kItems], (it / kItems) & 1);
       const int* const pos = ctl->pos[it % kItems];
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       auto muls = [&](int u, int i) -> uint64_t {
         return kRegs ? pair(qm[kRegs ? i : 0], qm[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(qmul + row_of(u) + i);
       };
-      if (softmax_any(over())) break;
+      softmax_sync();
 #pragma unroll 1
       for (int n = 0; n < n_here; ++n, ++ti) {
         const uint32_t sbuf = ts + (ti & 1) * C::kSCols;
@@ -845,6 +851,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     for (uint32_t it = 0;; ++it) {
       const Item& x_ = item_at(it);
       const int R = x_.R, flags = x_.flags, r_item = x_.rt * TM, hq0 = x_.h * A.G;
+      if (epilogue_any(over() || x_.n_tiles == 0)) break;
       const int NH = (R + 7) / 8;
       const int64_t row0 = x_.row0;
       const bool complete = (flags & 3) == 3;
@@ -864,10 +871,19 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       const float unit = ctl->unit[it & 1];
-      if (epilogue_any(over())) break;
+      epilogue_sync();
       wait(&ctl->o_full[it % C::kOBufs], (it / C::kOBufs) & 1);
       tc_fence_after();
       uint32_t bad[2] = {0, 0};
+      uint16_t* orow;      // row h * 8 of the output, or of the partial
+      float* prow = part + d;
+      int hq;
+      {
+        const int t = token_of(A, r_item);
+        hq = r_item - t * A.G;
+        orow = A.out + (row0 + t) * A.ldo + (int64_t)(hq0 + hq) * D + d;
+      }
+      const int64_t step = A.ldo - (int64_t)A.G * D;  // behind a token's last head
 #pragma unroll 1
       for (int h = 0; h < NH; ++h) {
         float o[8], y[8], z[8];
@@ -878,24 +894,40 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         wait_ld8(o);
         wait_ld8(y);
         if (F8) wait_ld8(z);
-        int t = token_of(A, r_item + h * 8), hq = r_item + h * 8 - t * A.G;
+        uint64_t zero = 0;  // sum of 0 * output: NaN if one is not finite
+        float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = h * 8 + i;
-          if (r < R) {
-            const float fr = ctl->out_fac[r];
-            float v = (F8 ? fmaf(z[i], 0x1p-8f, fmaf(y[i], 0x1p-4f, o[i])) : o[i] + y[i]) * unit;
-            if (fr == 0.f) v = 0.f;  // sees no key
-            if (writes) {
-              if (!(fabsf(v) < INFINITY)) bad[r >> 5] |= 1u << (r & 31);
-              if (complete) A.out[(row0 + t) * A.ldo + (int64_t)(hq0 + hq) * D + d] = (uint16_t)pk2<DT>(v * fr, 0.f);
-              else part[(size_t)r * D + d] = v;
+        for (int i = 0; i < 8; i += 2) {
+          const uint64_t lo = F8 ? fma2(pair(z[i], z[i + 1]), pair(0x1p-4f, 0x1p-4f), pair(y[i], y[i + 1])) : pair(y[i], y[i + 1]);
+          const uint64_t all = F8 ? fma2(lo, pair(0x1p-4f, 0x1p-4f), pair(o[i], o[i + 1])) : add2(lo, pair(o[i], o[i + 1]));
+          unpair(*reinterpret_cast<const uint64_t*>(ctl->out_fac + h * 8 + i), f[i], f[i + 1]);
+          unpair(mul2(all, pair(unit, unit)), o[i], o[i + 1]);
+          o[i] = f[i] == 0.f || h * 8 + i >= R ? 0.f : o[i];  // sees no key, or is no row
+          o[i + 1] = f[i + 1] == 0.f || h * 8 + i + 1 >= R ? 0.f : o[i + 1];
+          zero = fma2(pair(o[i], o[i + 1]), pair(0.f, 0.f), zero);
+        }
+        float z0, z1;
+        unpair(zero, z0, z1);
+        if (writes && z0 + z1 != 0.f) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!(fabsf(o[i]) < INFINITY)) bad[h >> 2] |= 1u << ((h & 3) * 8 + i);
+        }
+        if (complete) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (writes && h * 8 + i < R) *orow = (uint16_t)pk2<DT>(o[i] * f[i], 0.f);
+            orow += D;
+            if (++hq == A.G) {
+              hq = 0;
+              orow += step;
             }
           }
-          if (++hq == A.G) {
-            hq = 0;
-            ++t;
-          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (writes && h * 8 + i < R) prow[i * D] = o[i];
+          prow += 8 * D;
         }
       }
       tc_fence_before();
