@@ -1322,7 +1322,7 @@ slora_status_t slora_kv_attention(slora_pool* P, const slora_kv_layout_t* layout
   A.G = n_q_heads / layout->n_kv_heads;
   divide_by(A.G, A.g_mul, A.g_shift);  // rows: at most 2^20 tokens of 2^10 heads
   A.c = (float)((double)scale * 1.4426950408889634);
-  A.window = window;
+  A.window = window < (1 << 30) ? window : 0;  // no position is 2^30 or more
   A.max_rows = std::min(max_rows, T);
   A.workspace = workspace;
   A.chunk_workspace = static_cast<char*>(workspace) + kv_stream_workspace(layout->format, layout->head_dim, P->sm_count);

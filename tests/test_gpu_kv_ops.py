@@ -497,6 +497,16 @@ def test_rows_that_see_nothing_beside_infinities(group, fmt):
     _compare(c, qv, out, lse, 2 * group, once=True)
 
 
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1, (1 << 30) - 1])
+def test_the_largest_windows_beside_rows_before_the_first_token(window):
+    c = Cache([(6, 4), (1, 300), (40, 33)], 2, 64, "bf16", 0, 4096)
+    c.fill()
+    qv, q = _q(c, 4)
+    out, lse = _attend(c, q, 4, window=window)
+    assert c.check()[0] == 0
+    _compare(c, qv, out, lse, 4, once=True)
+
+
 @pytest.mark.parametrize("group,n", [(1, 1), (8, 2), (8, 40)])
 def test_attention_where_every_sequence_fits_one_tile(group, n):
     """A table of at most 128 positions, at 128 and below: nothing is joined."""
