@@ -306,37 +306,66 @@ __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* worksp
   const int r_item = sp.rt * TM, R = min(s.n * A.G - r_item, TM);
   auto at = [&](int i) { return parts + (size_t)(i == 0 ? sp.slot : 2 * (run + i)) * slot_floats(TM, D); };
   for (int r = blockIdx.y * (kCombineThreads / 32) + warp; r < R; r += gridDim.y * (kCombineThreads / 32)) {
-    float top = -INFINITY;
-    for (int i = lane; i < sp.n; i += 32) top = fmaxf(top, at(i)[(size_t)TM * D + r]);
+    // values of kAhead partials at a time; the first ones' loads are under way beside those of the statistics
+    constexpr int kAhead = 8;
+    float v[kAhead][E];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float* const p = at(min(i0 + k, sp.n - 1)) + (size_t)r * D + lane * E;
+        if (E == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(p);
+          v[k][0] = x.x;
+          v[k][1] = x.y;
+          v[k][E - 2] = x.z;
+          v[k][E - 1] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(p);
+          v[k][0] = x.x;
+          v[k][1] = x.y;
+        }
+      }
+    };
+    load(0);
+    float m0 = -INFINITY, l0 = 0.f;
+    if (lane < sp.n) {
+      m0 = at(lane)[(size_t)TM * D + r];
+      l0 = at(lane)[(size_t)TM * (D + 1) + r];
+    }
+    float top = m0;
+    for (int i = lane + 32; i < sp.n; i += 32) top = fmaxf(top, at(i)[(size_t)TM * D + r]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
     const float z = top == -INFINITY ? 0.f : top;
     float l = 0.f, o[E] = {};
+#pragma unroll 1
     for (int i0 = 0; i0 < sp.n; i0 += 32) {
-      float w = 0.f, li = 0.f;
-      if (i0 + lane < sp.n) {
-        w = ex2(at(i0 + lane)[(size_t)TM * D + r] - z);
-        li = w * at(i0 + lane)[(size_t)TM * (D + 1) + r];
+      if (i0 > 0) {
+        m0 = -INFINITY;
+        l0 = 0.f;
+        if (i0 + lane < sp.n) {
+          m0 = at(i0 + lane)[(size_t)TM * D + r];
+          l0 = at(i0 + lane)[(size_t)TM * (D + 1) + r];
+        }
       }
+      const float w = ex2(m0 - z);
+      l += w * l0;
       const int n = min(32, sp.n - i0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(FULL_MASK, w, i);
-        l += __shfl_sync(FULL_MASK, li, i);
-        const float* p = at(i0 + i) + (size_t)r * D + lane * E;
-        if (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(p);
-          o[0] += wi * v.x;
-          o[1] += wi * v.y;
-          o[E - 2] += wi * v.z;
-          o[E - 1] += wi * v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(p);
-          o[0] += wi * v.x;
-          o[1] += wi * v.y;
+#pragma unroll 1
+      for (int j = 0; j < n; j += kAhead) {
+        if (i0 + j > 0) load(i0 + j);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float wk = __shfl_sync(FULL_MASK, w, (j + k) & 31);
+          if (j + k < n) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += wk * v[k][e];
+          }
         }
       }
     }
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(FULL_MASK, l, k);
     const float inv = inverse(l);
     const int t = token_of(A, r_item + r), hq = sp.h * A.G + (r_item + r) - t * A.G;
     const int64_t tok = s.row0 + t;
