@@ -40,11 +40,12 @@
 //         K's row scale multiplies the score, V's the weight, relative to twice the largest V scale
 //         met so far.
 //
-// Measured: 256 tokens of 32 heads (one row a kv head) over 200..2000 keys, 3.24 GB in fp16: 488 us, 6.6 TB/s;
-// one token, 64 heads on 8, over 130001 keys, bf16: 93 us, 5.7 TB/s (of which 90 in this kernel, at 5.9); 64 tokens,
-// 64 heads on 8, over 1000..16000 keys in e4m3, 0.7 GB: 128 us, 5.5 TB/s.  With up to 16 rows HBM's pace is
-// 1400 cycles a tile of e4m3 and the softmax's 1100 to 1300; with 40 rows the softmax takes 4000.  The copies
-// go at 7.0 TB/s by themselves (16-byte cp.async, four warps); TMA's row gather brings 1.9, a bulk copy per 1 KB 3.6.
+// Measured (three inputs in turn): 256 tokens of 32 heads (one row a kv head) over 200..2000 keys, 3.24 GB in
+// fp16: 507 us, 6.4 TB/s; one token, 64 heads on 8, over 130001 keys, bf16: 91 us, 5.8 TB/s (85 in this kernel, at
+// 6.2); 64 tokens, 64 heads on 8, over 1000..16000 keys in e4m3, 0.7 GB: 145 us, 4.8 TB/s: at 8 rows the
+// copies' issue, the softmax and HBM take about 1370 cycles each for a tile; with 40 rows the softmax takes 4000.
+// The copies go at 7.0 TB/s by themselves (16-byte cp.async, four warps); TMA's row gather brings 1.9, a bulk copy
+// per 1 KB 3.6.
 //
 // A key that a row does not see has weight 0, but 0 * inf is NaN: where a
 // masked V row holds an infinity or a NaN, the rows that it spoiled are seen to be not
