@@ -86,7 +86,9 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {  // a in the 
 __device__ __forceinline__ uint2 quantise8(const float* f, RowScale s) {
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = f[i] * s.rinv;
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 x, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 r, {%4, %4};\n\tmul.rn.f32x2 x, x, r;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(q[i]), "=f"(q[i + 1]) : "f"(f[i]), "f"(f[i + 1]), "f"(s.rinv));
   if (s.exact) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = fmaf(-fmaf(q[i], s.scale, -f[i]), s.rinv, q[i]);  // (signs that keep -0)
@@ -137,6 +139,21 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_write(KvDev P, const uint16_
 #pragma unroll
       for (int i = 0; i < kIter; ++i) x[i] = next[i];
       if (r0 - lane / LPR + kIter * RPI < end) load(r0 + kIter * RPI);
+      uint32_t tops[kIter / 2];  // the rows' largest magnitudes, as 16-bit patterns
+      if (FMT == SLORA_KV_E4M3) {
+#pragma unroll
+        for (int i = 0; i < kIter; i += 2) {
+          uint32_t t[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            t[k] = max_u16x2(max_u16x2(x[i + k].x & 0x7fff7fffu, x[i + k].y & 0x7fff7fffu),
+                             max_u16x2(x[i + k].z & 0x7fff7fffu, x[i + k].w & 0x7fff7fffu));
+          uint32_t top = max_u16x2(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[0], t[1], 0x7632));
+#pragma unroll
+          for (int o = LPR / 2; o >= 1; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(FULL_MASK, top, o));
+          tops[i / 2] = top;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
         const int r = r0 + i * RPI;
@@ -144,12 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_write(KvDev P, const uint16_
         if (FMT == SLORA_KV_16) {
           if (r < end) *reinterpret_cast<uint4*>(to + (int64_t)off * kRowBytes) = x[i];
         } else {
-          // the largest magnitude, as a 16-bit pattern
-          uint32_t top = max_u16x2(max_u16x2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                   max_u16x2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-#pragma unroll
-          for (int o = LPR / 2; o >= 1; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(FULL_MASK, top, o));
-          top = max(top & 0xffff, top >> 16);
+          const uint32_t top = i & 1 ? tops[i / 2] >> 16 : tops[i / 2] & 0xffff;
           float scale = 0.f;
           uint2 codes = make_uint2(0, 0);
           if (top >= (DT == SLORA_BF16 ? 0x7f80u : 0x7c00u)) {
