@@ -134,19 +134,24 @@ struct Cursor {
   }
 };
 
-// a * b / c; the line is short enough for 32 bits nearly always.
-__device__ __forceinline__ long long share(long long a, int b, int c) {
-  if (a < (1 << 20) && b < (1 << 11)) return (uint32_t)a * (uint32_t)b / (uint32_t)c;
-  return a * b / c;
-}
+// The cut of the line: runs of q + 1 units, `rem` of them, then runs of q.
+struct Cut {
+  long long q, u1;  // u1: the end of this CTA's run
+  int rem;
+  __device__ long long start(int run) const { return run * q + min(run, rem); }
+  __device__ int run_of(long long unit) const {
+    const long long edge = rem * (q + 1), x = unit < edge ? unit : unit - edge, d = unit < edge ? q + 1 : q;
+    const int i = x < (1ll << 32) && d < (1ll << 32) ? (int)((uint32_t)x / (uint32_t)d) : (int)(x / d);
+    return unit < edge ? i : rem + i;
+  }
+};
 
 // This CTA's run of the line, found by one warp (some 400 instructions: 20 warps of a CTA that all
 // went through them spent 4500 cycles), a lane adding up some neighbouring
 // sequences.  Runs are at least E + min_tiles units, so that each has a tile.
-// False: this CTA has none.  total, ctas, u1: units in the line, runs, this run's end.
+// False: this CTA has none.
 template <int TM, int TK, int E>
-__device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_tiles, Cursor<TM, TK, E>& c,
-                                         long long& total, int& ctas, long long& u1) {
+__device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int min_tiles, Cursor<TM, TK, E>& c, Cut& cut) {
   const int lane = threadIdx.x & 31, B = A.kv.B, per = (B + 31) >> 5, b0 = lane * per;
   long long mine = 0;
 #pragma unroll 4
@@ -158,17 +163,20 @@ __device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int m
     const long long y = __shfl_up_sync(FULL_MASK, inc, o);
     if (lane >= o) inc += y;
   }
-  total = __shfl_sync(FULL_MASK, inc, 31);
-  ctas = (int)min((long long)gridDim.x, total < (1ll << 31) ? (long long)((uint32_t)total / (uint32_t)(E + min_tiles)) : total);
-  ctas = max(ctas, total > 0 ? 1 : 0);
-  if ((int)blockIdx.x >= ctas) return false;
-  const long long u0 = share(total, blockIdx.x, ctas);
-  u1 = share(total, blockIdx.x + 1, ctas);
+  const long long total = __shfl_sync(FULL_MASK, inc, 31);
+  const bool small = total < (1ll << 31);
+  const long long most = small ? (uint32_t)total / (uint32_t)(E + min_tiles) : total;
+  const int ctas = max((int)min((long long)gridDim.x, most), total > 0 ? 1 : 0), run = blockIdx.x;
+  if (run >= ctas) return false;
+  cut.q = small ? (uint32_t)total / (uint32_t)ctas : total / ctas;
+  cut.rem = (int)(total - cut.q * ctas);
+  const long long u0 = cut.start(run);
+  cut.u1 = cut.start(run + 1);
   // the sequence that holds unit u0 (there is one: u0 < total)
   long long off = u0 - (inc - mine);
   const int src = __ffs(__ballot_sync(FULL_MASK, off >= 0 && off < mine)) - 1;
   int b = b0;
-  if (lane == src) {
+  if (lane == src && per > 1) {
     for (;; ++b) {
       const long long w = seq_units<TM, TK, E>(A, cls, b);
       if (off < w) break;
@@ -176,7 +184,7 @@ __device__ __forceinline__ bool find_run(const KvAttnDev& A, RowClass cls, int m
     }
   }
   c.seek(A, cls, __shfl_sync(FULL_MASK, b, src), __shfl_sync(FULL_MASK, off, src));
-  c.left = u1 - u0;
+  c.left = cut.u1 - u0;
   return true;
 }
 
@@ -209,17 +217,14 @@ __device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK,
   return x;
 }
 
-// Partials of an item whose first tile is in this run (slot: this CTA's) and
-// whose last one is unit end - 1 of the line.
-__device__ __forceinline__ void note_split(Split* sp, int b, int h, int rt, int slot, long long end, long long total,
-                                           int ctas) {
-  // the run of unit end - 1
-  const long long x = end * ctas + total - 1, last = (x < (1ll << 32) ? (uint32_t)x / (uint32_t)total : x / total) - 1;
-  sp->b = b;
-  sp->h = h;
-  sp->rt = rt;
+// Partials of the item at c, whose first tile is in this run (slot: this CTA's).
+template <int TM, int TK, int E>
+__device__ __forceinline__ void note_split(Split* sp, const Cursor<TM, TK, E>& c, const Cut& cut, int slot) {
+  sp->b = c.b;
+  sp->h = c.h;
+  sp->rt = c.rt;
   sp->slot = slot;
-  sp->n = (int)(last - blockIdx.x) + 1;
+  sp->n = cut.run_of(cut.u1 - c.left + (c.size() - c.at) - 1) - (int)blockIdx.x + 1;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -197,9 +197,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
     if (warp == 13) {
       // ------------------------------------------------------ the run's items
       Cursor<kTM, kTK, kLead> c;
-      long long total, u1;
-      int ctas;
-      const bool any = find_run<kTM, kTK, kLead>(A, cls, kMinRun, c, total, ctas, u1);
+      Cut cut;
+      const bool any = find_run<kTM, kTK, kLead>(A, cls, kMinRun, c, cut);
       if (lane == 0) {
         if (!any) {
           ctl->item[0].n_tiles = 0;
@@ -207,11 +206,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         } else {
           for (uint32_t it = 0;; ++it) {
             const Item x = item_of(A, c);
-            if ((x.flags & 3) == 1)
-              note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
             wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
             ctl->item[it % kItems] = x;
             arrive(&ctl->item_full[it % kItems]);
+            if ((x.flags & 3) == 1) note_split(split, c, cut, 2 * blockIdx.x + (it > 0 ? 1 : 0));
             if ((x.flags & 4) || !c.next(A, cls)) break;
           }
         }

@@ -389,9 +389,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       // 130, 128; 2, 4 tiles: a mixed step with items of 40 rows 145, 142.
       constexpr int E = TM <= 16 ? 1 : 3;
       Cursor<TM, kTK, E> c;
-      long long total, u1;
-      int ctas;
-      const bool any = find_run<TM, kTK, E>(A, cls, kMinRun, c, total, ctas, u1);
+      Cut cut;
+      const bool any = find_run<TM, kTK, E>(A, cls, kMinRun, c, cut);
       if (lane == 0) {
         if (!any) {
           ctl->item[0].n_tiles = 0;
@@ -399,11 +398,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         } else {
           for (uint32_t it = 0;; ++it) {
             const Item x = item_of(A, c);
-            if ((x.flags & 3) == 1)
-              note_split(split, c.b, c.h, c.rt, 2 * blockIdx.x + (it > 0 ? 1 : 0), u1 - c.left + (c.size() - c.at), total, ctas);
             wait(&ctl->item_empty[it % kItems], ((it / kItems) & 1) ^ 1);
             ctl->item[it % kItems] = x;
             arrive(&ctl->item_full[it % kItems]);
+            if ((x.flags & 3) == 1) note_split(split, c, cut, 2 * blockIdx.x + (it > 0 ? 1 : 0));
             if ((x.flags & 4) || !c.next(A, cls)) break;
           }
         }
