@@ -486,7 +486,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
 #pragma unroll 1
         for (int n = 0; n < n_tiles; ++n, ++ti, ++sn) {
           const uint32_t g = 2 * ti + 1;
-          wait(&ctl->kv_full[g % S], (g / S) & 1);  // scales and mask
+          // Scales and mask.  The scores first: a group that passed over an item would find V's barrier two
+          // phases behind, which looks like done; with these scores issued, the phase before is over.
+          wait(&ctl->s_full[wg][0], sn & 1);
+          wait(&ctl->kv_full[g % S], (g / S) & 1);
           const float* const ks = scales + (ti % kMeta) * 2 * kTK;
           const int key0 = (tile0 + n) * kTK;
           const uint4 have = *reinterpret_cast<const uint4*>(ctl->mask[ti % kMeta]);
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
 #pragma unroll 1
           for (int part = 0; part < kParts; ++part) {
             const uint32_t ts = tq + part * kPart;
-            wait(&ctl->s_full[wg][part], sn & 1);
+            if (part > 0) wait(&ctl->s_full[wg][part], sn & 1);
             tc_fence_after();
             float s[kPart];
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

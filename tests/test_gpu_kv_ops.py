@@ -497,6 +497,24 @@ def test_rows_that_see_nothing_beside_infinities(group, fmt):
     _compare(c, qv, out, lse, 2 * group, once=True)
 
 
+@pytest.mark.parametrize("fmt,D", [(0, 128), (1, 128), (0, 64)])
+@pytest.mark.parametrize("lens", [[(1292, 1684), (1377, 1773), (1484, 1893), (1413, 1851)], [(90, 300), (97, 220), (130, 480)] * 5])
+def test_chunks_whose_last_row_tile_is_small(lens, fmt, D):
+    """Row tiles of 256 rows and one of 14 to 143 in turn, over keys that end inside a tile: one softmax group passes
+    over the small ones and comes to the next item before its barriers are there."""
+    torch = _torch()
+    H, group = 8, 3
+    c = Cache(lens, H, D, "bf16", fmt, 2048)
+    c.fill()
+    qv, q = _q(c, H * group)
+    out, lse = _attend(c, q, H * group)
+    assert c.check()[0] == 0
+    _compare(c, qv, out, lse, H * group, seqs=[0, 2], once=True)
+    for _ in range(10):
+        again, lse2 = _attend(c, q, H * group)
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1, (1 << 30) - 1])
 def test_the_largest_windows_beside_rows_before_the_first_token(window):
     c = Cache([(6, 4), (1, 300), (40, 33)], 2, 64, "bf16", 0, 4096)
