@@ -11,8 +11,8 @@
 // launch and a chain of three dependent loads).  A warp takes rows of one token,
 // kIter * 32 / (D / 8) at a time; the first ones' loads are issued before the token's page is
 // looked up, so that the look-up's latency hides behind them.
-// Measured: a prefill step's 24,888 tokens of 32 kv heads of 128 into e4m3 pages, 618 MB: 130 us (4.8 TB/s;
-// 120 instructions per 16 bytes and lane, 69 % of the issue slots); 8 heads, 11,935 tokens as they are, 98 MB: 19 us;
+// Measured: a prefill step's 24,888 tokens of 32 kv heads of 128 into e4m3 pages, 618 MB: 119 us (5.2 TB/s;
+// instruction issue, then HBM); 8 heads, 11,935 tokens as they are, 98 MB: 19 us;
 // reading 24,273 tokens of 32 heads, 795 MB: 135 us (5.9 TB/s); one token: 4 us.
 #include "kv_common.cuh"
 
