@@ -404,7 +404,9 @@ slora_status_t slora_kv_read(slora_pool* pool, const slora_kv_layout_t* layout, 
  * (natural; T x n_q_heads fp32 contiguous; may be NULL).  A row that sees no key
  * gets 0 and -inf.  Keys that a row does not see have no influence on it,
  * whatever their bits.  q, out: T x n_q_heads*head_dim, not overlapping.  Sums and
- * statistics are fp32, out is rounded once.
+ * statistics are fp32, out is rounded once; the weights meet V as two 16-bit halves
+ * each (a 16-bit cache and at most 32 rows, tokens times query heads of a kv head,
+ * in the sequence), as one 16-bit value (more rows), or as their fp16 value (e4m3).
  *   - max_rows: a host-side bound on the rows of any one sequence (longer ones
  *     are skipped, code 8): 1 for a decode step, T where nothing is known;
  *   - workspace: slora_kv_attention_workspace_bytes() bytes of device memory,
