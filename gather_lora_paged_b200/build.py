@@ -34,7 +34,7 @@ def _stale():
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return OUT
-    cmd = [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
+    cmd = [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "--threads", "0", "-Xcompiler", "-fPIC,-O2",
            "-shared", "-cudart", "static", "-I" + os.path.join(ROOT, "include"),
            *sources(), "-o", OUT + ".tmp"]
     if verbose:
