@@ -24,8 +24,9 @@
 // rounded once to the operand type, which puts an error of the size of the output's own
 // rounding on it (the two halves of kv_decode.cu would double the P.V
 // product, which is half the work here).
-// e4m3: K's scale multiplies the score, V's the weight, relative to twice the largest
-// V scale met so far.
+// e4m3: K's scale multiplies the score, V's the weight, over a unit (a power of two) of each row's own, so that
+// keys that a row does not see have no part in it: the largest product of weight and scale that the row
+// has met is 2^7..2^8 units where the unit is set, and 2^15 at most before it moves.
 //
 // What bounds it: both products of a tile take 2100 cycles (128 columns and 16 elements 64), the
 // exponentials of its 256 x 128 weights as long on the special-function units; a tile takes 3300, as
@@ -52,6 +53,9 @@ constexpr int kLead = 2;      // an item's lead: q and the outputs cost about tw
 constexpr int kItems = 4;     // items that are known ahead
 constexpr int kMeta = 8;      // tiles whose scales and masks are kept
 constexpr float kSlack = 8.f; // log2 of the largest weight
+// e4m3: log2 of the largest weight where a unit is set, and of what it may grow to (fp16 ends at 2^16)
+constexpr int kSet = 7;
+constexpr float kMost = 0x1p15f;
 
 template <int FMT, int D>
 struct Cfg {
@@ -478,7 +482,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         const int low = A.window > 0 && r < R ? pos - A.window : -1;   // keys above it are seen
         const int pmin = first + token_of(A, r_item + wg * 128);       // of the first row of this q tile
         const int pmax = first + token_of(A, r_item + R - 1);
-        float m = -INFINITY, l = 0.f, vn = 0.f, cr = A.c;
+        float m = -INFINITY, l = 0.f, cr = A.c;
+        float unit = -126.f, inv_unit = 0x1p126f;  // e4m3: log2 of the unit of this row's weights
         if (F8) {
           wait(&ctl->rows_full[it % kItems], (it / kItems) & 1);
           cr = qscale[(it % kItems) * kTM + r];
@@ -495,16 +500,6 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           const uint4 have = *reinterpret_cast<const uint4*>(ctl->mask[ti % kMeta]);
           const bool masked = key0 + kTK - 1 > pmin || (A.window > 0 && key0 <= pmax - A.window) ||
                               (have.x & have.y & have.z & have.w) != FULL_MASK;
-          float ratio = 1.f;
-          if (F8) {
-            const float4 v4 = *reinterpret_cast<const float4*>(ks + kTK + lane * 4);
-            const float tv = warp_max(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)));
-            if (tv > vn || n == 0) {
-              const float v = fmaxf(2.f * tv, 0x1p-126f);
-              ratio = vn / v;
-              vn = v;
-            }
-          }
 #pragma unroll 1
           for (int part = 0; part < kParts; ++part) {
             const uint32_t ts = tq + part * kPart;
@@ -546,67 +541,92 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
                 for (int q = 0; q < 4; ++q) top[q] = max3(top[q], s[i + 2 * q], s[i + 2 * q + 1]);
               }
             }
-            const float mn = fmaxf(m, fmaxf(max3(top[0], top[1], top[2]), top[3]) * cr);
-            if (__any_sync(FULL_MASK, mn > m + kSlack) || (F8 && ratio != 1.f)) {
+            float mn = fmaxf(m, fmaxf(max3(top[0], top[1], top[2]), top[3]) * cr);
+            float f = 1.f;  // what scales the products so far
+            if (__any_sync(FULL_MASK, mn > m + kSlack)) {
+              // e4m3: a whole number, so that a reference moves beside the unit without a rounding of either
+              if (F8) mn = ceilf(mn);
               const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
+              if (F8 && mn != -INFINITY) {
+                const float keep = unit + (m - mn);
+                unit = fmaxf(keep, -126.f);
+                f = unit == keep || m == -INFINITY ? 1.f : ex2(keep - unit);
+                inv_unit = __int_as_float((127 - (int)unit) << 23);
+              }
+              if (!F8) f = a;
               m = mn;
               l *= a;
-              if (n > 0 || part > 0) {
-                wait(&ctl->pv_done[wg], (pv + 1) & 1);  // the products so far
-                tc_fence_after();
-                const float f = a * ratio;
-#pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                  float o[32];
-                  ld32(to + i, o);
-                  wait_ld32(o);
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) o[k] *= f;
-                  st32(to + i, o);
-                }
-              }
-              ratio = 1.f;
             }
             const float mz = m == -INFINITY ? 0.f : m;
-            const float vinv = F8 ? __frcp_rn(vn) : 1.f;
-            const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz), vi2 = pair(vinv, vinv);
+            const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz);
             uint64_t ls[2] = {0, 0};
-            auto weigh = [&](auto all_seen) {  // the weights, from the scores
-              constexpr bool kOpen = decltype(all_seen)::value;
+            if (F8) {  // weights times V's scales, over the scores
+              float most[2] = {0.f, 0.f};
+              auto scale_v = [&](auto all_seen) {
+                constexpr bool kOpen = decltype(all_seen)::value;
 #pragma unroll
-              for (int i = 0; i < kPart; i += 32) {
-                uint32_t w[16];
+                for (int i = 0; i < kPart; i += 2) {
+                  float p[2], q[2];
+                  unpair(fma2(pair(s[i], s[i + 1]), c2, m2), p[0], p[1]);
+                  const uint64_t pp = pair(ex2(p[0]), ex2(p[1]));
+                  ls[(i >> 1) & 1] = add2(ls[(i >> 1) & 1], pp);
+                  unpair(mul2(pp, *reinterpret_cast<const uint64_t*>(kh + kTK + i)), q[0], q[1]);
+                  if (!kOpen) {  // an infinite or NaN scale of an unseen key stays out
+                    q[0] = s[i] == -INFINITY ? 0.f : q[0];
+                    q[1] = s[i + 1] == -INFINITY ? 0.f : q[1];
+                  }
+                  s[i] = q[0];
+                  s[i + 1] = q[1];
+                  most[(i >> 1) & 1] = max3(most[(i >> 1) & 1], q[0], q[1]);
+                }
+              };
+              if (masked) scale_v(std::false_type{});
+              else scale_v(std::true_type{});
+              const float big = fmaxf(most[0], most[1]);
+              if (big * inv_unit > kMost) {  // the unit moves: to this row's largest so far
+                const float to_unit = fminf((float)((__float_as_int(big) >> 23) - 127 - kSet), 126.f);
+                f *= ex2(unit - to_unit);
+                unit = to_unit;
+                inv_unit = __int_as_float((127 - (int)unit) << 23);
+              }
+            }
+            if ((n > 0 || part > 0) && __any_sync(FULL_MASK, f != 1.f)) {
+              wait(&ctl->pv_done[wg], (pv + 1) & 1);  // the products so far
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 32) {
+                float o[32];
+                ld32(to + i, o);
+                wait_ld32(o);
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                  float p[2];
+                for (int k = 0; k < 32; ++k) o[k] *= f;
+                st32(to + i, o);
+              }
+            }
+            const uint64_t iu2 = pair(inv_unit, inv_unit);
+#pragma unroll
+            for (int i = 0; i < kPart; i += 32) {  // the weights
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                float p[2];
+                if (F8) {
+                  unpair(mul2(pair(s[i + k], s[i + k + 1]), iu2), p[0], p[1]);
+                } else {
                   unpair(fma2(pair(s[i + k], s[i + k + 1]), c2, m2), p[0], p[1]);
                   p[0] = ex2(p[0]);
                   p[1] = ex2(p[1]);
-                  uint64_t pp = pair(p[0], p[1]);
-                  ls[(k >> 1) & 1] = add2(ls[(k >> 1) & 1], pp);
-                  if (F8) {
-                    pp = mul2(pp, mul2(*reinterpret_cast<const uint64_t*>(kh + kTK + i + k), vi2));
-                    float q[2];
-                    unpair(pp, q[0], q[1]);
-                    if (!kOpen) {  // a NaN scale of an unseen key stays out
-                      q[0] = p[0] == 0.f ? 0.f : q[0];
-                      q[1] = p[1] == 0.f ? 0.f : q[1];
-                    }
-                    w[k / 2] = pk2<MT>(q[0], q[1]);
-                  } else {
-                    w[k / 2] = pk2<MT>(p[0], p[1]);
-                  }
+                  ls[(k >> 1) & 1] = add2(ls[(k >> 1) & 1], pair(p[0], p[1]));
                 }
-                st16(ts + i / 2, w);
-                if (i % 64 == 32) {  // the products with these 64 keys may begin
-                  wait_st();
-                  tc_fence_before();
-                  arrive(&ctl->p_full[wg][part + i / 64]);
-                }
+                w[k / 2] = pk2<MT>(p[0], p[1]);
               }
-            };
-            if (F8 && masked) weigh(std::false_type{});
-            else weigh(std::true_type{});
+              st16(ts + i / 2, w);
+              if (i % 64 == 32) {  // the products with these 64 keys may begin
+                wait_st();
+                tc_fence_before();
+                arrive(&ctl->p_full[wg][part + i / 64]);
+              }
+            }
             pv += kPart / 64;
             float a, b;
             unpair(add2(ls[0], ls[1]), a, b);
@@ -624,7 +644,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         uint16_t* const orow = A.out + tok * A.ldo + (int64_t)hq * D;
         float* const part = parts + (size_t)(2 * blockIdx.x + (it > 0 ? 1 : 0)) * slot_floats(kTM, D);
         float* const prow = part + (size_t)r * D;
-        const float f = (F8 ? vn : 1.f), f1 = complete ? inv : 1.f;
+        const float f = F8 ? 1.f / inv_unit : 1.f, f1 = complete ? inv : 1.f;
         bool bad = false;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {

@@ -27,7 +27,7 @@
 //   warps 16..19  an item's end: O^T from TMEM to the output, beside the next item.
 //
 // Weights are exp(s - m) with m a former maximum of the row: it moves (and O^T is
-// scaled) only when a score exceeds it by 2^8 (16-bit) or 2^5 (e4m3), which one vote per tile finds out.
+// scaled) only when a score exceeds it by 2^8, which one vote per tile finds out.
 //
 // What the tensor cores take is split so that nothing is lost that an output could show:
 // 16-bit: weights as hi + lo, two 16-bit columns of N.
@@ -35,10 +35,11 @@
 //         are sums of three e4m3 values, each 2^-4 of the one before and a
 //         column of its own: 12 bits, so an fp16 q is exact, and a weight is its fp16 value.  The
 //         largest of a q row lies in [2^7, 2^8) after a power of two, what is lost of any element is under
-//         2^-26 of it; the weights are 2^3 at m and 2^8 at most, what is lost of each is under 2^-11 of
-//         it or 2^-21 of the row's largest (as fp32 pieces 2^-12, for a tenth of the time of a tile).
-//         K's row scale multiplies the score, V's the weight, relative to twice the largest V scale
-//         met so far.
+//         2^-26 of it.  K's row scale multiplies the score, V's the weight, over a unit (a power of two) of
+//         each row's own: the largest product of weight and scale that the row has met is 2^2..2^3 units where the
+//         unit is set, and 2^8 at most before it moves.  So keys that a row does not see have no part in it, and
+//         what is lost of a weight is under 2^-11 of it or 2^-20 of the row's largest with V's scales (as
+//         fp32 pieces 2^-12, for a tenth of the time of a tile).
 //
 // Measured (three inputs in turn): 256 tokens of 32 heads (one row a kv head) over 200..2000 keys, 3.24 GB in
 // fp16: 507 us, 6.4 TB/s; one token, 64 heads on 8, over 130001 keys, bf16: 91 us, 5.8 TB/s (85 in this kernel, at
@@ -69,9 +70,12 @@ constexpr float kNoRef = 0x1.fffffep127f;  // (negated) reference of a row that 
 template <int FMT, int D, int TM>
 struct Cfg {
   static constexpr bool kF8 = FMT == SLORA_KV_E4M3;
-  // log2 by which scores may exceed the row's reference, and the weight at the reference: weights of
-  // up to 2^13 (fp16 ends at 2^16) and 2^8 (e4m3 ends at 2^8.8)
-  static constexpr float kSlack = kF8 ? 5.f : 8.f, kLift = kF8 ? 8.f : 32.f;
+  // log2 by which scores may exceed the row's reference, and in e4m3 of the largest weight (e4m3 ends at 2^8.8)
+  static constexpr float kSlack = 8.f;
+  // 16-bit: the weight at the reference, so that weights are up to 2^13 (fp16 ends at 2^16)
+  static constexpr float kLift = 32.f;
+  // e4m3: log2 of the largest weight where a unit is set
+  static constexpr float kSet = 3.f;
   static constexpr int kRow = KvRow<FMT, D>::kBytes;                    // a cached row
   static constexpr int kWidth = kRow >= 128 ? 128 : kRow;               // bytes of a row in a panel
   static constexpr int kPanel = kTK * kWidth;
@@ -105,11 +109,15 @@ struct Ctl {
   uint32_t mask[kMeta][4];                    // keys of a tile that are there
   alignas(16) float qmul[kItems][(TM + 15) / 16 * 16];    // score multipliers of an item's rows
   int pos[kItems][(TM + 15) / 16 * 16];       // their positions (-1: no such row)
-  float red[4][TM + 4];                       // warps' maxima
+  float red[2][4][TM];                        // warps' maxima, of scores and (e4m3) with V's scales
   alignas(16) float ref[TM];                  // the rows' references, negated
-  float fac[TM];                              // what a move of them scales sums by
-  // an item's end, for the epilogue: warps' sums, references, the weights' unit, and its own notes
-  float sum[2][4][TM], end_ref[2][TM], unit[2];
+  // e4m3: one over the units of their weights, and the reference (negated) of a score with log2 of V's scale
+  alignas(16) float inv[TM];
+  alignas(16) float vref[TM];
+  float fac[TM], ofac[TM];                    // what a move of these scales sums and products by
+  // an item's end, for the epilogue: warps' sums, references, the weights' units, and its own notes
+  float sum[2][4][TM], end_ref[2][TM];
+  alignas(8) float unit[2][TM];
   alignas(8) float out_fac[TM];
   uint32_t bad[4][2];                         // warps' rows that are not finite
 };
@@ -600,7 +608,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     // references and score multipliers: in registers where there are few
     constexpr bool kRegs = NU == 1;
     constexpr float kSlack = C::kSlack, kLift = C::kLift;
-    float mr[kRegs ? UN : 1] = {}, qm[kRegs ? UN : 1] = {};
+    float mr[kRegs ? UN : 1] = {}, qm[kRegs ? UN : 1] = {}, iu[kRegs ? UN : 1] = {}, mv[kRegs ? UN : 1] = {};
     auto refs = [&](int u, int i) -> uint64_t {  // of rows i, i + 1
       return kRegs ? pair(mr[kRegs ? i : 0], mr[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(ctl->ref + row_of(u) + i);
     };
@@ -614,19 +622,30 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       const int* const pos = ctl->pos[it % kItems];
       const float* const qmul = ctl->qmul[it % kItems];
       const int pmin = pos[0], pmax = pos[R - 1];
-      float vn = 0.f;
 #pragma unroll
       for (int r = 0; r < NU * UN; ++r) l[r] = 0.f;
-      if (tid < TM) ctl->ref[tid] = kNoRef;
+      if (tid < TM) {
+        ctl->ref[tid] = kNoRef;
+        ctl->inv[tid] = 0x1p126f;
+        ctl->vref[tid] = kNoRef;
+      }
       if (kRegs) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
           mr[kRegs ? i : 0] = kNoRef;
+          iu[kRegs ? i : 0] = 0x1p126f;
+          mv[kRegs ? i : 0] = kNoRef;
           if (F8) qm[kRegs ? i : 0] = qmul[row_of(0) + i];
         }
       }
       auto muls = [&](int u, int i) -> uint64_t {
         return kRegs ? pair(qm[kRegs ? i : 0], qm[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(qmul + row_of(u) + i);
+      };
+      auto invs = [&](int u, int i) -> uint64_t {
+        return kRegs ? pair(iu[kRegs ? i : 0], iu[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(ctl->inv + row_of(u) + i);
+      };
+      auto vrefs = [&](int u, int i) -> uint64_t {
+        return kRegs ? pair(mv[kRegs ? i : 0], mv[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(ctl->vref + row_of(u) + i);
       };
       softmax_sync();
 #pragma unroll 1
@@ -649,6 +668,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         const int key0 = (tile0 + n) * kTK, j = key0 + key;
         const bool open = have == FULL_MASK && key0 + kTK - 1 <= pmin && (A.window <= 0 || key0 > pmax - A.window);
         const bool mine = (have >> lane) & 1;
+        const float lv = F8 ? __log2f(vs) : 0.f;
         float s[NU * UN];
         float most = -INFINITY;  // over the references
 #pragma unroll
@@ -689,42 +709,49 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               float a, b;
               unpair(add2(pair(x[i], x[i + 1]), refs(u, i)), a, b);
               most = max3(most, a, b);
+              if (F8) {
+                unpair(add2(add2(pair(x[i], x[i + 1]), pair(lv, lv)), vrefs(u, i)), a, b);
+                most = max3(most, a, b);
+              }
             }
           }
         }
-        if (softmax_any(most > kSlack || (F8 && mine && vs > vn))) {  // some reference moves: to the tile's maxima
+        if (softmax_any(most > kSlack)) {  // some reference moves to its tile's maximum, or a unit to its tile's largest weight
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
             if (row_of(u) < R) {
 #pragma unroll
               for (int i = 0; i < UN; ++i) {
-                const float v = warp_max(s[u * UN + i]);
-                if (lane == 0) ctl->red[wk][row_of(u) + i] = v;
+                const float x = s[u * UN + i], v = warp_max(x);
+                if (lane == 0) ctl->red[0][wk][row_of(u) + i] = v;
+                if (F8) {
+                  const float w = warp_max(x == -INFINITY ? x : x + lv);
+                  if (lane == 0) ctl->red[1][wk][row_of(u) + i] = w;
+                }
               }
             }
           }
-          if (F8 && half == 0) {
-            const float v = warp_max(mine ? vs : 0.f);
-            if (lane == 0) ctl->red[wk][TM] = v;
-          }
           softmax_sync();
-          float ratio = 1.f;
-          if (F8) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) v = fmaxf(v, ctl->red[w][TM]);
-            if (v > vn) {
-              v = fmaxf(2.f * v, 0x1p-126f);
-              ratio = vn / v;
-              vn = v;
-            }
-          }
           if (tid < (R + UN - 1) / UN * UN) {
             const int r = tid;
-            const float top = fmaxf(fmaxf(ctl->red[0][r], ctl->red[1][r]), fmaxf(ctl->red[2][r], ctl->red[3][r]));
-            const float m = ctl->ref[r], m1 = top + m > kSlack ? -top : m;  // negated
+            auto top_of = [&](int k) {
+              return fmaxf(fmaxf(ctl->red[k][0][r], ctl->red[k][1][r]), fmaxf(ctl->red[k][2][r], ctl->red[k][3][r]));
+            };
+            const float top = top_of(0), m = ctl->ref[r];  // negated
+            // e4m3: a whole number, so that a reference moves beside a unit without a rounding of either
+            const float m1 = top + m > kSlack ? (F8 ? -ceilf(top) : -top) : m;
             ctl->fac[r] = m1 == m ? 1.f : ex2(m1 - m);
             ctl->ref[r] = m1;
+            if (F8) {
+              const bool none = m == kNoRef;
+              const float e = (float)(127 - (__float_as_int(ctl->inv[r]) >> 23));  // log2 of the unit
+              const float keep = none ? -INFINITY : e + (m1 - m), need = top_of(1) + m1;
+              float e1 = need - keep > kSlack ? ceilf(need) - C::kSet : keep;
+              e1 = fminf(fmaxf(e1, -126.f), 126.f);
+              ctl->ofac[r] = none || e1 == keep ? 1.f : ex2(keep - e1);
+              ctl->inv[r] = __int_as_float((127 - (int)e1) << 23);
+              ctl->vref[r] = m1 - e1;
+            }
           }
           if (n > 0) {  // the products so far
             wait(&ctl->pv_done[(ti - 1) & 1], ((ti - 1) >> 1) & 1);
@@ -739,11 +766,14 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               bool same = true;
 #pragma unroll
               for (int i = 0; i < UN; ++i) {
-                const float a = ctl->fac[r0 + i];
-                l[u * UN + i] *= a;
-                f[i] = a * ratio;
+                l[u * UN + i] *= ctl->fac[r0 + i];
+                f[i] = F8 ? ctl->ofac[r0 + i] : ctl->fac[r0 + i];
                 same &= f[i] == 1.f;
                 if (kRegs) mr[kRegs ? i : 0] = ctl->ref[r0 + i];
+                if (F8 && kRegs) {
+                  iu[kRegs ? i : 0] = ctl->inv[r0 + i];
+                  mv[kRegs ? i : 0] = ctl->vref[r0 + i];
+                }
               }
               if (n > 0 && !same) {
 #pragma unroll 1
@@ -762,8 +792,6 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
         // the weights of tile ti - 2 have been used: its products were issued before these scores
         const uint32_t pd = sb + C::kOffP + (ti & 1) * C::kP + key * 16;
-        // relative V scale; no weight exceeds 2^8, and an infinite scale makes a NaN
-        const float f = F8 ? vs * __frcp_rn(fmaxf(vn, 0x1p-126f)) * kLift : kLift;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           const int r0 = row_of(u);
@@ -772,22 +800,21 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 #pragma unroll
             for (int i = 0; i < UN; i += 2) {
               const float* const x = s + u * UN + i;
-              float p[2];
-              unpair(add2(pair(x[0], x[1]), refs(u, i)), p[0], p[1]);
-              p[0] = ex2(p[0]);
-              p[1] = ex2(p[1]);
-              const uint64_t pp = pair(p[0], p[1]);
-              unpair(add2(pair(l[u * UN + i], l[u * UN + i + 1]), pp), l[u * UN + i], l[u * UN + i + 1]);
-              unpair(mul2(pp, pair(f, f)), p[0], p[1]);
-              if (F8) {
-                if (!open) {  // a NaN scale of an unseen key stays out
-                  p[0] = x[0] == -INFINITY ? 0.f : p[0];
-                  p[1] = x[1] == -INFINITY ? 0.f : p[1];
+              float a, b;
+              unpair(add2(pair(x[0], x[1]), refs(u, i)), a, b);
+              const uint64_t pp = pair(ex2(a), ex2(b));
+              if (F8) {  // (p * vs first: no factor of it is out of range where the weight is not)
+                unpair(mul2(mul2(pp, pair(vs, vs)), invs(u, i)), a, b);
+                if (!open) {  // an infinite or NaN scale of an unseen key stays out
+                  a = x[0] == -INFINITY ? 0.f : a;
+                  b = x[1] == -INFINITY ? 0.f : b;
                 }
-                split3_weights(pair(p[0], p[1]), w[0][i / 2], w[1][i / 2], w[2][i / 2]);
+                split3_weights(pair(a, b), w[0][i / 2], w[1][i / 2], w[2][i / 2]);
               } else {
-                split2<DT>(p[0], p[1], w[0][i / 2], w[1][i / 2]);
+                unpair(mul2(pp, pair(kLift, kLift)), a, b);
+                split2<DT>(a, b, w[0][i / 2], w[1][i / 2]);
               }
+              unpair(add2(pair(l[u * UN + i], l[u * UN + i + 1]), pp), l[u * UN + i], l[u * UN + i + 1]);
             }
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
@@ -833,8 +860,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           if (lane % (32 / UN) == 0) ctl->sum[it & 1][wk][row_of(u) + lane / (32 / UN)] = v[0];
         }
       }
-      if (tid < TM) ctl->end_ref[it & 1][tid] = ctl->ref[tid] == kNoRef ? -INFINITY : -ctl->ref[tid];
-      if (tid == 0) ctl->unit[it & 1] = (F8 ? vn : 1.f) * (1.f / C::kLift);
+      if (tid < TM) {
+        ctl->end_ref[it & 1][tid] = ctl->ref[tid] == kNoRef ? -INFINITY : -ctl->ref[tid];
+        ctl->unit[it & 1][tid] = F8 ? 1.f / ctl->inv[tid] : 1.f / C::kLift;
+      }
       arrive(&ctl->sum_full[it & 1]);
       if (flags & 4) break;
     }
@@ -869,7 +898,6 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           part[(size_t)TM * (D + 1) + r] = lr;
         }
       }
-      const float unit = ctl->unit[it & 1];
       epilogue_sync();
       wait(&ctl->o_full[it % C::kOBufs], (it / C::kOBufs) & 1);
       tc_fence_after();
@@ -900,7 +928,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           const uint64_t lo = F8 ? fma2(pair(z[i], z[i + 1]), pair(0x1p-4f, 0x1p-4f), pair(y[i], y[i + 1])) : pair(y[i], y[i + 1]);
           const uint64_t all = F8 ? fma2(lo, pair(0x1p-4f, 0x1p-4f), pair(o[i], o[i + 1])) : add2(lo, pair(o[i], o[i + 1]));
           unpair(*reinterpret_cast<const uint64_t*>(ctl->out_fac + h * 8 + i), f[i], f[i + 1]);
-          unpair(mul2(all, pair(unit, unit)), o[i], o[i + 1]);
+          unpair(mul2(all, *reinterpret_cast<const uint64_t*>(ctl->unit[it & 1] + h * 8 + i)), o[i], o[i + 1]);
           o[i] = f[i] == 0.f || h * 8 + i >= R ? 0.f : o[i];  // sees no key, or is no row
           o[i + 1] = f[i + 1] == 0.f || h * 8 + i + 1 >= R ? 0.f : o[i + 1];
           zero = fma2(pair(o[i], o[i + 1]), pair(0.f, 0.f), zero);
