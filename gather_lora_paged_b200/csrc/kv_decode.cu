@@ -31,15 +31,14 @@
 //
 // What the tensor cores take is split so that nothing is lost that an output could show:
 // 16-bit: weights as hi + lo, two 16-bit columns of N.
-// e4m3:   the codes are operands as they are (kind::f8f6f4), and q and the weights
-//         are sums of three e4m3 values, each 2^-4 of the one before and a
-//         column of its own: 12 bits, so an fp16 q is exact, and a weight is its fp16 value.  The
+// e4m3:   the codes are operands as they are (kind::f8f6f4).  q is a sum of three e4m3 values, each 2^-4 of
+//         the one before and a column of its own: 12 bits, so an fp16 q is exact; the
 //         largest of a q row lies in [2^7, 2^8) after a power of two, what is lost of any element is under
-//         2^-26 of it.  K's row scale multiplies the score, V's the weight, over a unit (a power of two) of
-//         each row's own: the largest product of weight and scale that the row has met is 2^2..2^3 units where the
+//         2^-26 of it.  A weight is its fp16 value, as a sum of four e4m3 values, each 2^-5 of the one before.
+//         K's row scale multiplies the score, V's the weight, over a unit (a power of two) of
+//         each row's own: the largest product of weight and scale that the row has met is 2^3..2^4 units where the
 //         unit is set, and 2^8 at most before it moves.  So keys that a row does not see have no part in it, and
-//         what is lost of a weight is under 2^-11 of it or 2^-20 of the row's largest with V's scales (as
-//         fp32 pieces 2^-12, for a tenth of the time of a tile).
+//         what is lost of a weight is under 2^-11 of it or 2^-28 of the row's largest with V's scales.
 //
 // Measured (three inputs in turn): 256 tokens of 32 heads (one row a kv head) over 200..2000 keys, 3.24 GB in
 // fp16: 507 us, 6.4 TB/s; one token, 64 heads on 8, over 130001 keys, bf16: 91 us, 5.8 TB/s (85 in this kernel, at
@@ -75,17 +74,17 @@ struct Cfg {
   // 16-bit: the weight at the reference, so that weights are up to 2^13 (fp16 ends at 2^16)
   static constexpr float kLift = 32.f;
   // e4m3: log2 of the largest weight where a unit is set
-  static constexpr float kSet = 3.f;
+  static constexpr float kSet = 4.f;
   static constexpr int kRow = KvRow<FMT, D>::kBytes;                    // a cached row
   static constexpr int kWidth = kRow >= 128 ? 128 : kRow;               // bytes of a row in a panel
   static constexpr int kPanel = kTK * kWidth;
   static constexpr int kSlot = kTK * kRow;                              // K or V of a tile
   static constexpr int kRows16 = (TM + 15) / 16 * 16;
   static constexpr int kQRows = kF8 ? 3 * kRows16 : kRows16;            // columns of S^T
-  static constexpr int kPCols = kF8 ? 3 * kRows16 : 2 * TM;             // columns of O^T
+  static constexpr int kPCols = kF8 ? 4 * TM : 2 * TM;                  // columns of O^T
   static constexpr int kQ = kQRows * kRow;                              // one of two buffers
   static constexpr int kP = kPCols * (kF8 ? 1 : 2) * kTK;               // one of two buffers
-  static constexpr int kSlots = kF8 ? (D == 64 ? 16 : (TM <= 16 ? 10 : 8)) : (D == 64 ? 10 : (TM <= 16 ? 6 : 5));
+  static constexpr int kSlots = kF8 ? (D == 64 ? 16 : (TM <= 16 ? 10 : 7)) : (D == 64 ? 10 : (TM <= 16 ? 6 : 5));
   static constexpr int kOffP = kSlots * kSlot;
   static constexpr int kOffQ = kOffP + 2 * kP;
   static constexpr int kOffScale = kOffQ + 2 * kQ;
@@ -124,9 +123,6 @@ struct Ctl {
 
 __device__ __forceinline__ void st_shared8(uint32_t dst, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(a), "r"(b) : "memory");
-}
-__device__ __forceinline__ void st_shared4(uint32_t dst, uint32_t a) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(a) : "memory");
 }
 __device__ __forceinline__ void ld8(uint32_t taddr, float* v) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
@@ -187,20 +183,22 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low 
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-// Two weights as three e4m3 codes each, every one 2^-4 of the one before: of their fp16 values, whose 11 bits
-// they hold.
-__device__ __forceinline__ void split3_weights(uint64_t w, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+// Two weights of up to 2^8 as four e4m3 codes each, every one 2^-5 of the one before: exactly their fp16 values, the
+// least ones included (all of them have been tried; three codes at 2^-4 end at 2^-17, at 2^-5 at 2^-19).
+__device__ __forceinline__ void split4_weights(uint64_t w, uint32_t& p0, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
   float a, b;
   unpair(w, a, b);
   asm("{\n\t.reg .b32 h, c, s;\n\t.reg .b16 k;\n\t"
-      "mov.b32 s, 0x4c004c00;\n\t"                      // 16, 16
-      "cvt.rn.f16x2.f32 h, %4, %3;\n\t"
+      "mov.b32 s, 0x50005000;\n\t"                      // 32, 32
+      "cvt.rn.f16x2.f32 h, %5, %4;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %0, k;\n\tcvt.rn.f16x2.e4m3x2 c, k;\n\t"
       "sub.f16x2 h, h, c;\n\tmul.f16x2 h, h, s;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %1, k;\n\tcvt.rn.f16x2.e4m3x2 c, k;\n\t"
       "sub.f16x2 h, h, c;\n\tmul.f16x2 h, h, s;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %2, k;\n\t}"
-      : "=r"(p0), "=r"(p1), "=r"(p2) : "f"(a), "f"(b));
+      "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %2, k;\n\tcvt.rn.f16x2.e4m3x2 c, k;\n\t"
+      "sub.f16x2 h, h, c;\n\tmul.f16x2 h, h, s;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 k, h;\n\tcvt.u32.u16 %3, k;\n\t}"
+      : "=r"(p0), "=r"(p1), "=r"(p2), "=r"(p3) : "f"(a), "f"(b));
 }
 // Two values as three e4m3 codes each, every one 2^-4 of the one before.
 __device__ __forceinline__ void split3(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
@@ -552,7 +550,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               vleft = x.n_tiles;
               vlast = x.flags & 4;
               if (__any_sync(FULL_MASK, over())) break;
-              vn = F8 ? (x.R + 15) / 16 * 6 : (x.R + 7) / 8 * 2;
+              vn = !F8 ? (x.R + 7) / 8 * 2 : TM == 8 ? (x.R + 3) / 4 * 2 : (x.R + 7) / 8 * 4;
               first = true;
               obuf = (vit - 1) % C::kOBufs;
               wait(&ctl->o_empty[obuf], (((vit - 1) / C::kOBufs) & 1) ^ 1);
@@ -599,8 +597,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     const int half = warp >> 2, wk = warp & 3, key = tid & 127;
     auto row_of = [&](int u) { return TM == 8 ? half * 4 : (2 * u + half) * 8; };
     auto s_col = [&](int r0) { return F8 ? r0 / 16 * 48 + r0 % 16 : r0; };
-    auto o_col = [&](int r0) { return F8 ? r0 / 16 * 48 + r0 % 16 : r0 / 8 * 16 + r0 % 8; };
-    constexpr int PS = F8 ? 16 : 8, NP = F8 ? 3 : 2;  // columns from piece to piece of O^T, pieces
+    auto o_col = [&](int r0) { return F8 ? r0 * 4 : r0 / 8 * 16 + r0 % 8; };
+    constexpr int PS = F8 ? UN : 8, NP = F8 ? 4 : 2;  // columns from piece to piece of O^T, pieces
     const uint32_t tmem = tmem_at(), ts = tmem + ((uint32_t)(wk * 32) << 16);
     const float* const scales = reinterpret_cast<const float*>(smem + C::kOffScale);
     uint32_t ti = 0, vslot = 1, vphase = 0;
@@ -796,7 +794,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         for (int u = 0; u < NU; ++u) {
           const int r0 = row_of(u);
           if (r0 < R) {
-            uint32_t w[3][UN / 2];
+            uint32_t w[4][UN / 2];
 #pragma unroll
             for (int i = 0; i < UN; i += 2) {
               const float* const x = s + u * UN + i;
@@ -809,24 +807,29 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
                   a = x[0] == -INFINITY ? 0.f : a;
                   b = x[1] == -INFINITY ? 0.f : b;
                 }
-                split3_weights(pair(a, b), w[0][i / 2], w[1][i / 2], w[2][i / 2]);
+                split4_weights(pair(a, b), w[0][i / 2], w[1][i / 2], w[2][i / 2], w[3][i / 2]);
               } else {
                 unpair(mul2(pp, pair(kLift, kLift)), a, b);
                 split2<DT>(a, b, w[0][i / 2], w[1][i / 2]);
               }
               unpair(add2(pair(l[u * UN + i], l[u * UN + i + 1]), pp), l[u * UN + i], l[u * UN + i + 1]);
             }
+            if (F8) {  // a unit's columns in 16 bytes (4 rows) or twice 16
+              uint32_t c[8];
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-              if (!F8) {
+              for (int q = 0; q < 4; ++q) {
+                c[q * (UN / 4)] = w[q][0] | w[q][1] << 16;
+                if (UN == 8) c[2 * q + 1] = w[q][UN / 2 - 2] | w[q][UN / 2 - 1] << 16;
+              }
+              const uint32_t dst = pd + r0 / 4 * (kTK * 16);
+              st_shared16(dst, c[0], c[1], c[2], c[3]);
+              if (UN == 8) st_shared16(dst + kTK * 16, c[4], c[5], c[6], c[7]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < NP; ++q) {
                 const uint32_t dst = pd + (r0 / 8 * 2 + q) * (kTK * 16) + r0 % 8 * 2;
                 if (UN == 8) st_shared16(dst, w[q][0], w[q][1], w[q][UN / 2 - 2], w[q][UN / 2 - 1]);
                 else st_shared8(dst, w[q][0], w[q][1]);
-              } else {
-                const uint32_t dst = pd + (r0 / 16 * 3 + q) * (kTK * 16) + r0 % 16;
-                const uint32_t a = w[q][0] | w[q][1] << 16;
-                if (UN == 8) st_shared8(dst, a, w[q][UN / 2 - 2] | w[q][UN / 2 - 1] << 16);
-                else st_shared4(dst, a);
               }
             }
           }
@@ -913,20 +916,28 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       const int64_t step = A.ldo - (int64_t)A.G * D;  // behind a token's last head
 #pragma unroll 1
       for (int h = 0; h < NH; ++h) {
-        float o[8], y[8], z[8];
-        const uint32_t col = to + (F8 ? h / 2 * 48 + (h & 1) * 8 : h * 16);
-        ld8(col, o);
-        ld8(col + (F8 ? 16 : 8), y);
-        if (F8) ld8(col + 32, z);
-        wait_ld8(o);
-        wait_ld8(y);
-        if (F8) wait_ld8(z);
+        constexpr int NP = F8 ? 4 : 2;
+        float v[NP][8], o[8];
+        const uint32_t col = to + h * (8 * NP);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) ld8(col + 8 * q, v[q]);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) wait_ld8(v[q]);
+        auto piece = [&](int q, int i) {  // of rows i, i + 1 (8 rows a unit, or twice 4)
+          const int at = F8 && TM == 8 ? i / 4 * 16 + q * 4 + i % 4 : q * 8 + i;
+          return pair(v[at / 8][at % 8], v[at / 8][at % 8 + 1]);
+        };
         uint64_t zero = 0;  // sum of 0 * output: NaN if one is not finite
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const uint64_t lo = F8 ? fma2(pair(z[i], z[i + 1]), pair(0x1p-4f, 0x1p-4f), pair(y[i], y[i + 1])) : pair(y[i], y[i + 1]);
-          const uint64_t all = F8 ? fma2(lo, pair(0x1p-4f, 0x1p-4f), pair(o[i], o[i + 1])) : add2(lo, pair(o[i], o[i + 1]));
+          uint64_t all;
+          if constexpr (F8) {
+            const uint64_t s5 = pair(0x1p-5f, 0x1p-5f);
+            all = fma2(fma2(fma2(piece(3, i), s5, piece(2, i)), s5, piece(1, i)), s5, piece(0, i));
+          } else {
+            all = add2(piece(1, i), piece(0, i));
+          }
           unpair(*reinterpret_cast<const uint64_t*>(ctl->out_fac + h * 8 + i), f[i], f[i + 1]);
           unpair(mul2(all, *reinterpret_cast<const uint64_t*>(ctl->unit[it & 1] + h * 8 + i)), o[i], o[i + 1]);
           o[i] = f[i] == 0.f || h * 8 + i >= R ? 0.f : o[i];  // sees no key, or is no row

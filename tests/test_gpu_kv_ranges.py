@@ -1,5 +1,5 @@
 """Attention over KV pages where values lie far apart: V rows of very different sizes, seen and unseen;
-against the 64-bit definition.
+a key that takes nearly all of the weight; against the 64-bit definition.
 
 Tolerance, beside the terms of test_gpu_kv_ops.py for the output's rounding, the scores and the sums:
   p A           the weights' own rounding, p = 2^-11 for an 8-bit cache (their fp16 values), u for a 16-bit
@@ -17,7 +17,7 @@ import pytest
 
 import gather_lora_paged_b200 as G
 import kv_reference as R
-from test_gpu_kv_ops import U, Cache, _attend, _dev, _host
+from test_gpu_kv_ops import U, Cache, _attend, _dev, _host, _torch
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,42 @@ def test_v_rows_of_every_size(n, group, dtype):
     for b in (0, 1):
         rows = slice(b * n, b * n + n)
         _check(c, b, q[rows], out[rows], lse[rows], H * group, 1 / math.sqrt(D))
+
+
+def _one_key_above(L, n, group, dtype, fmt, gap, sink, B, D=64, H=1):
+    """B sequences over one cache of L tokens: key 0 is `gap` nats above all others, whose V rows have one sign."""
+    torch = _torch()
+    c = Cache([(n, L)], H, D, dtype, fmt, 65536, seed=L)
+
+    def spoil(b, part, x):
+        if part:
+            np.abs(x, out=x)
+            x[0] *= sink
+        else:
+            x *= 0.02
+            x[:, :, 0] = 0.0
+            x[0] = 0.0
+            x[0, :, 0] = 32.0
+    c.fill(spoil=spoil)
+    rng = np.random.default_rng(gap)
+    q = rng.standard_normal((n, H * group, D))
+    scale = 1 / math.sqrt(D)
+    q[:, :, 0] = gap / scale / 32.0
+    q = R.from_bits(R.to_bits(q, dtype), dtype)
+    one = c.lens[0]
+    c.lens, c.table, c.T = [one] * B, np.repeat(c.table, B, 0), n * B
+    c.starts = (np.arange(B + 1) * n).astype(np.int32)
+    c.upload()
+    dq = _dev(q.reshape(n, -1), dtype).repeat(B, 1)
+    out, lse = _attend(c, dq, H * group)
+    assert c.check()[0] == 0 and torch.isfinite(out).all()
+    return c, q, out, lse, scale
+
+
+@pytest.mark.parametrize("sink", [0.0, 2.0 ** -7, 1.0])
+@pytest.mark.parametrize("gap", [10, 14, 17])
+@pytest.mark.parametrize("n,group", [(1, 8), (2, 8), (5, 8)])
+def test_many_small_weights_beside_a_large_one_in_8_bits(n, group, gap, sink):
+    """8000 keys some 2^-20 below one: in a batch whose items are mostly not cut."""
+    c, q, out, lse, scale = _one_key_above(8000, n, group, "f16", 1, gap, sink, 160)
+    _check(c, 0, q, out, lse, group, scale)
