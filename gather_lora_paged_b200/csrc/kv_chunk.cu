@@ -17,9 +17,9 @@
 //               scores from TMEM, and writes the weights back over them in 16 bits; at the
 //               item's end it writes the row.
 // TMEM: S0, S1 (128 columns each, P over S), O0, O1 (D columns each).
-// The reference point of a row's weights (its maximum so far) moves only when the
-// maximum has grown by 2^8: weights then reach at most 2^8, far inside
-// fp16's range, and the accumulator in TMEM is read and scaled on few tiles.
+// The reference point of a row's weights (its maximum so far, less kLift) moves only when the
+// maximum has grown by 2^8, and the accumulator in TMEM is read and scaled on few tiles.  fp16 weights are 2^7
+// at the maximum, 2^15 at most, so that what falls below fp16's least step is under 2^-32 of the maximum's.
 // Sums and statistics are fp32 and of the unrounded weights; the weights are
 // rounded once to the operand type, which puts an error of the size of the output's own
 // rounding on it (the two halves of kv_decode.cu would double the P.V
@@ -52,7 +52,7 @@ constexpr int kMinRun = 2;
 constexpr int kLead = 2;      // an item's lead: q and the outputs cost about two tiles
 constexpr int kItems = 4;     // items that are known ahead
 constexpr int kMeta = 8;      // tiles whose scales and masks are kept
-constexpr float kSlack = 8.f; // log2 of the largest weight
+constexpr float kSlack = 8.f; // log2 by which a maximum may exceed the one that set the reference
 // e4m3: log2 of the largest weight where a unit is set, and of what it may grow to (fp16 ends at 2^16)
 constexpr int kSet = 7;
 constexpr float kMost = 0x1p15f;
@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   constexpr bool F8 = FMT == SLORA_KV_E4M3;
   constexpr int MT = F8 ? SLORA_F16 : DT;  // operand type of the products
   constexpr int S = C::kSlots, kPart = C::kPart, kParts = kTK / kPart;
+  constexpr float kLift = !F8 && MT == SLORA_F16 ? 7.f : 0.f;  // log2 of the weight at a row's maximum
   using Control = Ctl<S>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
                 for (int q = 0; q < 4; ++q) top[q] = max3(top[q], s[i + 2 * q], s[i + 2 * q + 1]);
               }
             }
-            float mn = fmaxf(m, fmaxf(max3(top[0], top[1], top[2]), top[3]) * cr);
+            float mn = fmaxf(m, fmaf(fmaxf(max3(top[0], top[1], top[2]), top[3]), cr, -kLift));
             float f = 1.f;  // what scales the products so far
             if (__any_sync(FULL_MASK, mn > m + kSlack)) {
               // e4m3: a whole number, so that a reference moves beside the unit without a rounding of either

@@ -146,3 +146,12 @@ def test_many_small_weights_beside_a_large_one_in_8_bits(n, group, gap, sink):
     """8000 keys some 2^-20 below one: in a batch whose items are mostly not cut."""
     c, q, out, lse, scale = _one_key_above(8000, n, group, "f16", 1, gap, sink, 160)
     _check(c, 0, q, out, lse, group, scale)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("gap,sink", [(14, 1.0), (17, 0.0), (18, 0.0), (19, 0.0)])
+@pytest.mark.parametrize("n,group", [(40, 2), (4, 8)])
+def test_many_small_weights_beside_a_large_one(n, group, gap, sink, fmt):
+    """As above for 16-bit caches and for many rows."""
+    c, q, out, lse, scale = _one_key_above(6000, n, group, "f16", fmt, gap, sink, 40)
+    _check(c, 0, q, out, lse, group, scale, once=n * group > 32)
