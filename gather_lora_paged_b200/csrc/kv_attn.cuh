@@ -1,6 +1,6 @@
 // kv_attn.cuh -- what the attention kernels share (kv_decode.cu,
 // kv_chunk.cu): the line of key tiles that is cut into one run per CTA, the
-// join of the partials, the row that is summed again.
+// join of the partials, V's values that are not finite.
 //
 // The rows of a kv head are the n * G pairs (token, head of the group), in row
 // tiles of TM.  A work item is (sequence, kv head, row tile); its keys come in
@@ -8,8 +8,16 @@
 // that ragged lengths and a single long sequence keep every SM equally busy.  An item is as long there as
 // its tiles and a lead of E units, for what it costs beside them (q, the first maximum, its
 // outputs).  An item inside one run is finished there; one that
-// crosses runs leaves (max, sum, unnormalised row) partials, at most two per
-// CTA, and k_kv_join joins them in key order.
+// crosses runs leaves (reference, sum, row) partials, at most two per
+// CTA, each row divided by its own sum, so that it is no larger than V; k_kv_join joins them in key order.
+//
+// The products meet all V rows of a tile, also those that some rows of the item do not see: with weight 0,
+// but 0 * inf is NaN.  So in tiles that cross an item's causal or window border the values of such keys that are not
+// finite are set to zero in shared memory before the products, and the item is marked (Item::odd).  Whatever
+// the values of V and the weights, no finite term overflows (the kernels' references see to that), so a sum that
+// is not finite comes from a value that is not: for such rows, and for those of marked items, settle() looks
+// up the keys that the row sees, and an output element with infinities of one sign becomes that infinity, one with
+// both signs or a NaN a NaN, whatever the products' pieces made of them.  It reads V once per warp and item.
 #pragma once
 
 #include <atomic>
@@ -195,8 +203,12 @@ struct Item {
   int lo, hi;             // keys some row sees
   int tile, n_tiles;      // this run's tiles of the item
   int flags;              // 1: it starts here, 2: it ends here, 4: the run's last
-  int pad;
+  int odd;                // a V row that some rows see and others do not held values that are not finite
+  int shut, late;         // keys above `shut`, or at `late` and below, are not seen by all rows
+  int pad[2];
 };
+
+constexpr int kNever = -(1 << 30);  // below every position, and that less a position is a number
 
 template <int TM, int TK, int E>
 __device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK, E>& c) {
@@ -213,7 +225,10 @@ __device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK,
   x.tile = c.x.t0 + first;
   x.n_tiles = end - E - first;
   x.flags = (first == 0 ? 1 : 0) | (end == c.size() ? 2 : 0) | (c.left - (end - c.at) <= E ? 4 : 0);
-  x.pad = 0;
+  x.odd = 0;
+  x.shut = x.first + token_of(A, x.rt * TM);
+  x.late = A.window > 0 ? x.first + token_of(A, x.rt * TM + x.R - 1) - A.window : kNever;
+  x.pad[0] = x.pad[1] = 0;
   return x;
 }
 
@@ -233,71 +248,173 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
+// 2^e, for a constant e.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 // 1 / sum, 0 for a row without keys (a NaN sum stays NaN).
 __device__ __forceinline__ float inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
 
-// One row of an item again, key by key, over keys [ka, kb) with the row's own
-// final maximum m: o_d = sum over visible keys of exp2(s_j - m) v_jd.  dst16 (a
-// finished row, divided by the sum l) or dst32 (a partial).  One warp; rare.
+// ---- values of V that are not finite
+
+// 16-bit values (of type DT), or e4m3 codes, with those that are not finite set to zero.
+template <bool CODES, int DT>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  if (CODES) return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  constexpr uint32_t kExp = DT == SLORA_BF16 ? 0x7f807f80u : 0x7c007c00u;
+  return w & ~__vcmpeq2(w & kExp, kExp);
+}
+// In a tile that has keys which some rows of the item do not see: their values that are not finite become zero, and
+// the item is marked, for a scale that is not finite too.  By the warp that issues the products, while it would wait
+// for the weights; chunk c of row k lies at at(k, c).  (In the softmax warps, which know these keys as well, the code alone
+// took 3 to 8 % of the calls' time.)
+template <bool CODES, int DT, int NC, typename At>
+__device__ __forceinline__ void clean_tile(Item* x, int key0, const float* scales, At at) {
+  const int lane = threadIdx.x & 31, shut = x->shut - key0, late = x->late - key0;
+  const int first = max(x->lo - key0, 0), end = min(x->hi - key0, kKvTile);
+  if (end - 1 <= shut && first > late) return;
+  bool odd = false;
+#pragma unroll 1
+  for (int k = first + lane; k < end; k += 32) {
+    if (k <= shut && k > late) continue;
+    if (scales != nullptr) odd |= !(fabsf(scales[k]) < INFINITY);
+#pragma unroll 4
+    for (int c = 0; c < NC; ++c) {
+      uint32_t w[4], f[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at(k, c)) : "memory");
+      uint32_t diff = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = finite_only<CODES, DT>(w[i]);
+        diff |= f[i] ^ w[i];
+      }
+      if (diff) {
+        odd = true;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, c)), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
+      }
+    }
+  }
+  if (odd) *reinterpret_cast<volatile int*>(&x->odd) = 1;
+  __syncwarp();  // (the issuing thread's fence towards the tensor cores follows; all lanes run it)
+}
+
+// Which of V's elements lane * E + e (E = D / 32) of keys [ka, kb) are not finite: bits 1 infinity, 2 -infinity,
+// 4 NaN, at 4 * e.  One warp.
 template <int DT, int FMT, int D>
-__device__ __noinline__ void redo_row(const KvAttnDev& A, int b, int h, const uint16_t* qrow, int p, int ka, int kb,
-                                      float m, float inv_l, uint16_t* dst16, float* dst32) {
-  constexpr int E = D / 32;  // values per lane
+__device__ __forceinline__ uint32_t odd_values(const KvAttnDev& A, int b, int h, int ka, int kb) {
+  constexpr int E = D / 32;
+  constexpr bool F8 = FMT == SLORA_KV_E4M3;
+  constexpr uint32_t kExp = DT == SLORA_BF16 ? 0x7f80u : 0x7c00u;
   const int lane = threadIdx.x & 31;
   const KvDev& P = A.kv;
-  float q[E], o[E];
+  const unsigned char* const base = reinterpret_cast<const unsigned char*>(P.pool) + lane * (F8 ? E : 2 * E);
+  uint32_t cls = 0;
+#pragma unroll 1
+  for (int j0 = ka; j0 < kb; j0 += 32) {
+    uint32_t row = j0 + lane < kb ? kv_row(P, b, j0 + lane, h) : kNoRow;
+    float scale = 1.f;
+    if (row != kNoRow) {
+      row += (uint32_t)(P.H * P.pt);
+      if (F8) scale = *kv_scale(P, row);
+    }
+    const unsigned odd_scales = F8 ? __ballot_sync(FULL_MASK, !(fabsf(scale) < INFINITY)) : 0;
+#pragma unroll 1
+    for (int k0 = 0; k0 < 32; k0 += 8) {  // 8 keys' loads under way at once
+      uint32_t w[8][2] = {};
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint32_t w = __ldg(qrow + lane * E + e);
-    float hi;
-    if (DT == SLORA_BF16) q[e] = __uint_as_float(w << 16);
-    else h2x2f(w, q[e], hi);
-    o[e] = 0.f;
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t r = __shfl_sync(FULL_MASK, row, k0 + k);
+        const unsigned char* const src = base + (uint64_t)r * KvRow<FMT, D>::kBytes;
+        if (r == kNoRow) continue;
+        if (!F8 && E == 4) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+          w[k][0] = x.x;
+          w[k][1] = x.y;
+        } else if (!F8 || E == 4) {
+          w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+        } else {
+          w[k][0] = __ldg(reinterpret_cast<const uint16_t*>(src));
+        }
+      }
+      uint32_t diff = odd_scales >> k0 & 0xff;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) diff |= (w[k][0] ^ finite_only<F8, DT>(w[k][0])) | (w[k][1] ^ finite_only<F8, DT>(w[k][1]));
+      if (!__any_sync(FULL_MASK, diff != 0)) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float s = F8 ? __shfl_sync(FULL_MASK, scale, k0 + k) : 1.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t v = F8 ? w[k][0] >> (8 * e) & 0xff : w[k][e >> 1] >> (16 * (e & 1)) & 0xffff;
+          uint32_t c = 0;
+          if (F8) {
+            if ((v & 0x7f) == 0x7f || s != s) c = 4;
+            else if (!(fabsf(s) < INFINITY)) c = (v & 0x7f) == 0 ? 4 : ((v >> 7) != 0) != (s < 0.f) ? 2 : 1;
+          } else if ((v & kExp) == kExp) {
+            c = (v & 0x7fff) != kExp ? 4 : v >> 15 ? 2 : 1;
+          }
+          cls |= c << (4 * e);
+        }
+      }
+    }
   }
-  if (A.window > 0) ka = max(ka, p - A.window + 1);
-  kb = min(kb, p + 1);
-  const unsigned char* base = reinterpret_cast<const unsigned char*>(P.pool);
-  for (int j = ka; j < kb; ++j) {
-    const uint32_t kr = kv_row(P, b, j, h);
-    if (kr == kNoRow) continue;
-    const uint32_t vr = kr + (uint32_t)(P.H * P.pt);
-    float kv[E], vv[E], dot = 0.f;
+  return cls;
+}
+
+// Puts in what V's values that are not finite make of rows r0 + i * step of an item, for the bits i of `rows` (see the top).
+// common: among the keys that all rows of the item see there may be some.  One warp.
+template <int DT, int FMT, int D, int TM>
+__device__ __forceinline__ void settle(const KvAttnDev& A, const Item& x, uint32_t rows, int r0, int step, bool common, float* part) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, r_item = x.rt * TM, b = x.b, h = x.h, W = A.window;
+  const int ka = max(x.tile * kKvTile, x.lo), kb = min((x.tile + x.n_tiles) * kKvTile, x.hi);
+  const bool odd = *reinterpret_cast<const volatile int*>(&x.odd), complete = (x.flags & 3) == 3;
+  const int ac = max(ka, x.late + 1), bc = min(kb, x.shut + 1);  // keys that all rows see
+  uint32_t all = 0, later = 0;  // of these keys, of those behind them up to `upto`
+  int upto = bc;
+  bool first = true;
+#pragma unroll 1
+  for (; rows; rows &= rows - 1, first = false) {
+    const int r = r0 + (__ffs(rows) - 1) * step, t = token_of(A, r_item + r), p = x.first + t;
+    const int from = W > 0 ? max(ka, p - W + 1) : ka, to = min(kb, p + 1);
+    uint32_t own = 0;
+#pragma unroll 1
+    for (int i = 0; i < 3; ++i) {  // the three parts of the keys that the row sees (one where no key is seen by all)
+      int k0 = ac, k1 = first && common ? bc : ac;
+      if (i == 1) {  // (rows in order: their positions do not fall)
+        k0 = upto;
+        k1 = odd ? to : upto;
+      } else if (i == 2) {
+        k0 = from;
+        k1 = odd ? min(ac, to) : from;
+      }
+      if (ac >= bc) {
+        k0 = from;
+        k1 = i == 2 ? to : from;
+      }
+      if (k0 >= k1) continue;
+      const uint32_t c = odd_values<DT, FMT, D>(A, b, h, k0, k1);
+      if (i == 0) all |= c;
+      else if (i == 1) later |= c;
+      else own |= c;
+      if (i == 1) upto = k1;
+    }
+    const uint32_t cls = all | later | own;
+    const int hq = x.h * A.G + (r_item + r) - t * A.G;
+    uint16_t* const o16 = A.out + (int64_t)(x.row0 + t) * A.ldo + (int64_t)hq * D + lane * E;
+    float* const o32 = part + (size_t)r * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      if (FMT == SLORA_KV_16) {
-        const uint32_t a = reinterpret_cast<const uint16_t*>(base)[(int64_t)kr * D + lane * E + e];
-        const uint32_t c = reinterpret_cast<const uint16_t*>(base)[(int64_t)vr * D + lane * E + e];
-        float hi;
-        if (DT == SLORA_BF16) {
-          kv[e] = __uint_as_float(a << 16);
-          vv[e] = __uint_as_float(c << 16);
-        } else {
-          h2x2f(a, kv[e], hi);
-          h2x2f(c, vv[e], hi);
-        }
-      } else {
-        const uint32_t a = e4m3x2_f16x2(base[(int64_t)kr * D + lane * E + e]);
-        const uint32_t c = e4m3x2_f16x2(base[(int64_t)vr * D + lane * E + e]);
-        kv[e] = __low2float(*reinterpret_cast<const __half2*>(&a)) * *kv_scale(P, kr);
-        vv[e] = __low2float(*reinterpret_cast<const __half2*>(&c)) * *kv_scale(P, vr);
-      }
-      dot += q[e] * kv[e];
+      const uint32_t c = cls >> (4 * e) & 7;
+      if (c == 0) continue;
+      const float v = c == 1 ? INFINITY : c == 2 ? -INFINITY : __uint_as_float(0x7fc00000u);
+      if (complete) o16[e] = (uint16_t)pack2<DT>(v, 0.f);
+      else o32[e] = v;
     }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, d);
-    const float w = ex2(dot * A.c - m);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += w * vv[e];
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (dst16) dst16[lane * E + e] = (uint16_t)pack2<DT>(o[e] * inv_l, 0.f);
-    else dst32[lane * E + e] = o[e];
   }
 }
 
 // Joins the partials of the item that starts in run `run` of a kernel's `ctas` and ends in a
-// later one: weights exp2(m_i - max m), in key order.  A warp per row.
+// later one: weights l_i exp2(m_i - max m), in key order; 2^-40 of that, so that no term overflows where V does
+// not.  A warp per row.
 constexpr int kCombineThreads = 256;
 template <int DT, int D, int TM>
 __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* workspace, int run, int ctas) {
@@ -341,7 +458,7 @@ __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* worksp
     for (int i = lane + 32; i < sp.n; i += 32) top = fmaxf(top, at(i)[(size_t)TM * D + r]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-    const float z = top == -INFINITY ? 0.f : top;
+    const float z = (top == -INFINITY ? 0.f : top) + 40.f;
     float l = 0.f, o[E] = {};
 #pragma unroll 1
     for (int i0 = 0; i0 < sp.n; i0 += 32) {
@@ -353,8 +470,8 @@ __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* worksp
           l0 = at(i0 + lane)[(size_t)TM * (D + 1) + r];
         }
       }
-      const float w = ex2(m0 - z);
-      l += w * l0;
+      const float w = ex2(m0 - z) * l0;
+      l += w;
       const int n = min(32, sp.n - i0);
 #pragma unroll 1
       for (int j = 0; j < n; j += kAhead) {
@@ -379,7 +496,7 @@ __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* worksp
       *reinterpret_cast<uint2*>(orow) = make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[E - 2] * inv, o[E - 1] * inv));
     else
       *reinterpret_cast<uint32_t*>(orow) = pack2<DT>(o[0] * inv, o[1] * inv);
-    if (A.lse && lane == 0) A.lse[tok * A.Hq + hq] = lse_of(top, l);
+    if (A.lse && lane == 0) A.lse[tok * A.Hq + hq] = lse_of(top, l * 0x1p40f);
   }
 }
 

@@ -138,7 +138,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
   constexpr bool F8 = FMT == SLORA_KV_E4M3;
   constexpr int MT = F8 ? SLORA_F16 : DT;  // operand type of the products
   constexpr int S = C::kSlots, kPart = C::kPart, kParts = kTK / kPart;
-  constexpr float kLift = !F8 && MT == SLORA_F16 ? 7.f : 0.f;  // log2 of the weight at a row's maximum
+  // log2 of the weight at a row's maximum.  fp16: weights are up to 2^15 (it ends at 2^16).  bf16: of 2^16
+  // keys at 2^8 over the maximum none of V's products and sums overflows, however large V is.
+  constexpr int kLift = F8 ? 0 : MT == SLORA_F16 ? 7 : -24;
   using Control = Ctl<S>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
@@ -272,6 +274,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           const bool more = n + 1 < n_tiles;
           const uint32_t v = (g + 1) % S, k = (g + 2) % S;
           wait(&ctl->kv_full[v], ((g + 1) / S) & 1);
+          clean_tile<false, MT, D / 8>(&ctl->item[it % kItems], (x.tile + n) * kTK,
+                                       F8 ? scales + (((g >> 1) % kMeta) * 2 + 1) * kTK : nullptr,
+                                       [&](int k, int c) { return sb + C::kOffRing + v * C::kSlot + place(k, c); });
           if (more) wait(&ctl->kv_full[k], ((g + 2) / S) & 1);
 #pragma unroll 1
           for (int step = 0; step < 2 * q_tiles; ++step) {  // in the order in which the weights come
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
                 for (int q = 0; q < 4; ++q) top[q] = max3(top[q], s[i + 2 * q], s[i + 2 * q + 1]);
               }
             }
-            float mn = fmaxf(m, fmaf(fmaxf(max3(top[0], top[1], top[2]), top[3]), cr, -kLift));
+            float mn = fmaxf(m, fmaf(fmaxf(max3(top[0], top[1], top[2]), top[3]), cr, -(float)kLift));
             float f = 1.f;  // what scales the products so far
             if (__any_sync(FULL_MASK, mn > m + kSlack)) {
               // e4m3: a whole number, so that a reference moves beside the unit without a rounding of either
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         uint16_t* const orow = A.out + tok * A.ldo + (int64_t)hq * D;
         float* const part = parts + (size_t)(2 * blockIdx.x + (it > 0 ? 1 : 0)) * slot_floats(kTM, D);
         float* const prow = part + (size_t)r * D;
-        const float f = F8 ? 1.f / inv_unit : 1.f, f1 = complete ? inv : 1.f;
+        const float f = F8 ? 1.f / inv_unit : 1.f;
         bool bad = false;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
@@ -654,10 +659,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           wait_ld32(o);
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
+            o[k] *= inv;
             if (F8) o[k] *= f;
             if (l == 0.f) o[k] = 0.f;  // sees no key
             bad |= !(fabsf(o[k]) < INFINITY);
-            o[k] *= f1;
           }
           if (r < R) {
             if (complete) {
@@ -673,28 +678,21 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           }
         }
         tc_fence_before();
+        const float m0 = m + kLift, l0 = l * pow2(-kLift);  // the maximum, the sum of weights of 1 there
         if (r < R) {
           if (complete) {
-            if (A.lse) A.lse[tok * A.Hq + hq] = lse_of(m, l);
+            if (A.lse) A.lse[tok * A.Hq + hq] = lse_of(m0, l0);
           } else {
-            part[(size_t)kTM * D + r] = m;
-            part[(size_t)kTM * (D + 1) + r] = l;
+            part[(size_t)kTM * D + r] = m0;
+            part[(size_t)kTM * (D + 1) + r] = l0;
           }
         }
-        unsigned again = __ballot_sync(FULL_MASK, bad && r < R && m != -INFINITY);
-#pragma unroll 1
-        while (again) {
-          __syncwarp();
-          const int src = __ffs(again) - 1;
-          again &= again - 1;
-          const int r2 = wg * 128 + (warp & 3) * 32 + src;
-          const int t2 = token_of(A, r_item + r2), hq2 = hq0 + (r_item + r2) - t2 * A.G;
-          const int64_t tok2 = row0 + t2;
-          redo_row<DT, FMT, D>(A, x.b, x.h, A.q + tok2 * A.ldq + (int64_t)hq2 * D, first + t2, max(tile0 * kTK, x.lo),
-                               min((tile0 + n_tiles) * kTK, x.hi), __shfl_sync(FULL_MASK, m, src),
-                               __shfl_sync(FULL_MASK, inv, src),
-                               complete ? A.out + tok2 * A.ldo + (int64_t)hq2 * D : nullptr, part + (size_t)r2 * D);
-        }
+        // rows that are not finite, or of a marked item; those that see no key, or whose sum is a NaN, are what
+        // they should be
+        const bool odd = *reinterpret_cast<const volatile int*>(&x.odd), common = __any_sync(FULL_MASK, bad && r < R);
+        const uint32_t rows = __ballot_sync(FULL_MASK, r < R && m != -INFINITY && l == l && (bad || odd));
+        __syncwarp();
+        if (__builtin_expect(rows != 0, 0)) settle<DT, FMT, D, kTM>(A, x, rows, wg * 128 + (warp & 3) * 32, 1, common, part);
       } else {
         ti += n_tiles;
       }

@@ -47,9 +47,7 @@
 // The copies go at 7.0 TB/s by themselves (16-byte cp.async, four warps); TMA's row gather brings 1.9, a bulk copy
 // per 1 KB 3.6.
 //
-// A key that a row does not see has weight 0, but 0 * inf is NaN: where a
-// masked V row holds an infinity or a NaN, the rows that it spoiled are seen to be not
-// finite at the end and are summed again key by key, without the masked keys.
+// Values of V that are not finite: kv_attn.cuh.
 #include <math.h>
 
 #include "kv_attn.cuh"
@@ -66,13 +64,14 @@ constexpr int kItems = 16;     // items that are known ahead
 constexpr float kNoRef = 0x1.fffffep127f;  // (negated) reference of a row that has seen no key
 
 // TM: rows per item.  N is a multiple of 16 rows (e4m3: three columns a row).
-template <int FMT, int D, int TM>
+template <int DT, int FMT, int D, int TM>
 struct Cfg {
   static constexpr bool kF8 = FMT == SLORA_KV_E4M3;
   // log2 by which scores may exceed the row's reference, and in e4m3 of the largest weight (e4m3 ends at 2^8.8)
   static constexpr float kSlack = 8.f;
-  // 16-bit: the weight at the reference, so that weights are up to 2^13 (fp16 ends at 2^16)
-  static constexpr float kLift = 32.f;
+  // 16-bit: log2 of the weight at a row's maximum.  fp16: weights are up to 2^13 (it ends at 2^16).  bf16: of 2^16
+  // keys at 2^8 over the maximum none of V's products and sums overflows, however large V is.
+  static constexpr int kLift = kF8 ? 0 : DT == SLORA_F16 ? 5 : -24;
   // e4m3: log2 of the largest weight where a unit is set
   static constexpr float kSet = 4.f;
   static constexpr int kRow = KvRow<FMT, D>::kBytes;                    // a cached row
@@ -221,7 +220,7 @@ __device__ __forceinline__ uint32_t place(int rows, int j, int c) {
 
 template <int DT, int FMT, int D, int TM>
 __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ KvAttnDev A, RowClass cls) {
-  using C = Cfg<FMT, D, TM>;
+  using C = Cfg<DT, FMT, D, TM>;
   constexpr int S = C::kSlots, W = C::kWidth;
   constexpr bool F8 = C::kF8;
   using Control = Ctl<TM, S>;
@@ -504,9 +503,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         const uint32_t k_lo = desc_lo(sb, 16), q_lo = desc_lo(sb + C::kOffQ, 16), v_lo = desc_lo(sb, C::kPanel);
         const uint32_t p_lo = desc_lo(sb + C::kOffP, 128);
         uint32_t qslot = 0, qphase = 0, qit = 0, vslot = 1, vphase = 0, vit = 0, obuf = 0;
-        int qleft = 0, vleft = 0, qn = 0, vn = 0;
+        int qleft = 0, vleft = 0, qn = 0, vn = 0, vkey = 0;
         int qlast = 0, vlast = 0;  // the item is the run's last
-        bool first = true;
+        bool first = true, vborder = false;  // (it has keys that not all rows see)
 #pragma unroll 1
         for (int step = 0;; ++step) {
           if (qleft > 0 || !qlast) {  // scores of tile `step`
@@ -549,6 +548,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               const Item& x = item_at(vit++);
               vleft = x.n_tiles;
               vlast = x.flags & 4;
+              vkey = x.tile * kTK;
+              vborder = x.hi - 1 > x.shut || x.lo <= x.late;
               if (__any_sync(FULL_MASK, over())) break;
               vn = !F8 ? (x.R + 7) / 8 * 2 : TM == 8 ? (x.R + 3) / 4 * 2 : (x.R + 7) / 8 * 4;
               first = true;
@@ -556,6 +557,12 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               wait(&ctl->o_empty[obuf], (((vit - 1) / C::kOBufs) & 1) ^ 1);
             }
             wait(&ctl->kv_full[vslot], vphase);
+            if (vborder)
+              clean_tile<F8, DT, C::kRow / 16>(
+                  &ctl->item[(vit - 1) % kItems], vkey,
+                  F8 ? reinterpret_cast<const float*>(smem + C::kOffScale) + ((ti % kMeta) * 2 + 1) * kTK : nullptr,
+                  [&](int k, int c) { return sb + vslot * C::kSlot + place<W>(kTK, k, c); });
+            vkey += kTK;
             wait(&ctl->p_full[ti & 1], (ti >> 1) & 1);
             fence_async_smem();
             tc_fence_after();
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
     float l[NU * UN];  // this key's sums
     // references and score multipliers: in registers where there are few
     constexpr bool kRegs = NU == 1;
-    constexpr float kSlack = C::kSlack, kLift = C::kLift;
+    constexpr float kSlack = C::kSlack, kLift = C::kLift;  // references lie kLift below the maximum
     float mr[kRegs ? UN : 1] = {}, qm[kRegs ? UN : 1] = {}, iu[kRegs ? UN : 1] = {}, mv[kRegs ? UN : 1] = {};
     auto refs = [&](int u, int i) -> uint64_t {  // of rows i, i + 1
       return kRegs ? pair(mr[kRegs ? i : 0], mr[kRegs ? i + 1 : 0]) : *reinterpret_cast<const uint64_t*>(ctl->ref + row_of(u) + i);
@@ -662,6 +669,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         if (F8) {
           ks = scales[(ti % kMeta) * 2 * kTK + key];
           vs = scales[((ti % kMeta) * 2 + 1) * kTK + key];
+          vs = fabsf(vs) < INFINITY ? vs : __uint_as_float(0x7fc00000u);  // (an e4m3 code of an infinity would be a number)
         }
         const int key0 = (tile0 + n) * kTK, j = key0 + key;
         const bool open = have == FULL_MASK && key0 + kTK - 1 <= pmin && (A.window <= 0 || key0 > pmax - A.window);
@@ -706,7 +714,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             for (int i = 0; i < UN; i += 2) {
               float a, b;
               unpair(add2(pair(x[i], x[i + 1]), refs(u, i)), a, b);
-              most = max3(most, a, b);
+              most = max3(most, a, b);  // (with kLift)
               if (F8) {
                 unpair(add2(add2(pair(x[i], x[i + 1]), pair(lv, lv)), vrefs(u, i)), a, b);
                 most = max3(most, a, b);
@@ -714,7 +722,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             }
           }
         }
-        if (softmax_any(most > kSlack)) {  // some reference moves to its tile's maximum, or a unit to its tile's largest weight
+        if (softmax_any(most > kSlack + kLift)) {  // some reference moves to its tile's maximum, or a unit to its tile's largest weight
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
             if (row_of(u) < R) {
@@ -737,7 +745,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
             };
             const float top = top_of(0), m = ctl->ref[r];  // negated
             // e4m3: a whole number, so that a reference moves beside a unit without a rounding of either
-            const float m1 = top + m > kSlack ? (F8 ? -ceilf(top) : -top) : m;
+            const float m1 = top + m > kSlack + kLift ? (F8 ? -ceilf(top) : kLift - top) : m;
             ctl->fac[r] = m1 == m ? 1.f : ex2(m1 - m);
             ctl->ref[r] = m1;
             if (F8) {
@@ -809,7 +817,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
                 }
                 split4_weights(pair(a, b), w[0][i / 2], w[1][i / 2], w[2][i / 2], w[3][i / 2]);
               } else {
-                unpair(mul2(pp, pair(kLift, kLift)), a, b);
+                unpair(pp, a, b);
                 split2<DT>(a, b, w[0][i / 2], w[1][i / 2]);
               }
               unpair(add2(pair(l[u * UN + i], l[u * UN + i + 1]), pp), l[u * UN + i], l[u * UN + i + 1]);
@@ -864,8 +872,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       if (tid < TM) {
-        ctl->end_ref[it & 1][tid] = ctl->ref[tid] == kNoRef ? -INFINITY : -ctl->ref[tid];
-        ctl->unit[it & 1][tid] = F8 ? 1.f / ctl->inv[tid] : 1.f / C::kLift;
+        ctl->end_ref[it & 1][tid] = ctl->ref[tid] == kNoRef ? -INFINITY : kLift - ctl->ref[tid];
+        if (F8) ctl->unit[it & 1][tid] = 1.f / ctl->inv[tid];
       }
       arrive(&ctl->sum_full[it & 1]);
       if (flags & 4) break;
@@ -893,12 +901,13 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         const int r = tl, t = token_of(A, r_item + r), hq = hq0 + (r_item + r) - t * A.G;
         const float (*const sum)[TM] = ctl->sum[it & 1];
         const float m = ctl->end_ref[it & 1][r], lr = (sum[0][r] + sum[1][r]) + (sum[2][r] + sum[3][r]);
-        ctl->out_fac[r] = complete ? inverse(lr) : lr == 0.f ? 0.f : 1.f;
+        const float l0 = lr * pow2(-C::kLift);  // of weights of 1 at the maximum
+        ctl->out_fac[r] = inverse(lr);
         if (complete) {
-          if (A.lse) A.lse[(row0 + t) * A.Hq + hq] = lse_of(m, lr);
+          if (A.lse) A.lse[(row0 + t) * A.Hq + hq] = lse_of(m, l0);
         } else {
           part[(size_t)TM * D + r] = m;
-          part[(size_t)TM * (D + 1) + r] = lr;
+          part[(size_t)TM * (D + 1) + r] = l0;
         }
       }
       epilogue_sync();
@@ -938,8 +947,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           } else {
             all = add2(piece(1, i), piece(0, i));
           }
-          unpair(*reinterpret_cast<const uint64_t*>(ctl->out_fac + h * 8 + i), f[i], f[i + 1]);
-          unpair(mul2(all, *reinterpret_cast<const uint64_t*>(ctl->unit[it & 1] + h * 8 + i)), o[i], o[i + 1]);
+          const uint64_t f2 = *reinterpret_cast<const uint64_t*>(ctl->out_fac + h * 8 + i);
+          unpair(f2, f[i], f[i + 1]);
+          all = mul2(all, f2);
+          if (F8) all = mul2(all, *reinterpret_cast<const uint64_t*>(ctl->unit[it & 1] + h * 8 + i));
+          unpair(all, o[i], o[i + 1]);
           o[i] = f[i] == 0.f || h * 8 + i >= R ? 0.f : o[i];  // sees no key, or is no row
           o[i + 1] = f[i + 1] == 0.f || h * 8 + i + 1 >= R ? 0.f : o[i + 1];
           zero = fma2(pair(o[i], o[i + 1]), pair(0.f, 0.f), zero);
@@ -954,7 +966,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         if (complete) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (writes && h * 8 + i < R) *orow = (uint16_t)pk2<DT>(o[i] * f[i], 0.f);
+            if (writes && h * 8 + i < R) *orow = (uint16_t)pk2<DT>(o[i], 0.f);
             orow += D;
             if (++hq == A.G) {
               hq = 0;
@@ -969,9 +981,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         }
       }
       tc_fence_before();
-      const bool spoiled = epilogue_any((bad[0] | bad[1]) != 0);
-      if (spoiled) {
-        // rows that are not finite: once more without the keys that they do not see
+      const bool odd = *reinterpret_cast<const volatile int*>(&x_.odd);
+      if (__builtin_expect(epilogue_any((bad[0] | bad[1]) != 0 || odd), 0)) {  // rows that are not finite, or of a marked item
         bad[0] = __reduce_or_sync(FULL_MASK, bad[0]);
         bad[1] = __reduce_or_sync(FULL_MASK, bad[1]);
         if (lane == 0) {
@@ -979,18 +990,16 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
           ctl->bad[wl][1] = bad[1];
         }
         epilogue_sync();
-#pragma unroll 1
-        for (int r = wl; r < R; r += 4) {
-          uint32_t any = 0;
+        uint32_t any[2];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) any |= ctl->bad[w][r >> 5];
-          if (!((any >> (r & 31)) & 1) || ctl->end_ref[it & 1][r] == -INFINITY) continue;
-          const int t = token_of(A, r_item + r), hq = hq0 + (r_item + r) - t * A.G;
-          redo_row<DT, FMT, D>(A, x_.b, x_.h, A.q + (row0 + t) * A.ldq + (int64_t)hq * D, x_.first + t,
-                               max(x_.tile * kTK, x_.lo), min((x_.tile + x_.n_tiles) * kTK, x_.hi), ctl->end_ref[it & 1][r],
-                               ctl->out_fac[r], complete ? A.out + (row0 + t) * A.ldo + (int64_t)hq * D : nullptr,
-                               part + (size_t)r * D);
-        }
+        for (int k = 0; k < 2; ++k) any[k] = ctl->bad[0][k] | ctl->bad[1][k] | ctl->bad[2][k] | ctl->bad[3][k];
+        const bool common = __any_sync(FULL_MASK, any[0] | any[1]);
+        // a warp's rows: wl, wl + 4, ...; those that see no key, or whose sum is a NaN, are what they should be
+        const int r = wl + 4 * lane;
+        const bool due = r < R && ctl->end_ref[it & 1][r] != -INFINITY && ctl->out_fac[r] == ctl->out_fac[r] &&
+                         (odd || (((r < 32 ? any[0] : any[1]) >> (r & 31)) & 1));
+        const uint32_t rows = __ballot_sync(FULL_MASK, due);
+        if (rows) settle<DT, FMT, D, TM>(A, x_, rows, wl, 4, common, part);
         epilogue_sync();
       }
       arrive(&ctl->o_empty[it % C::kOBufs]);
@@ -1006,7 +1015,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
 
 template <int DT, int FMT, int D, int TM>
 cudaError_t run_decode(const KvAttnDev& A, int sm_count, RowClass cls, cudaStream_t st) {
-  using C = Cfg<FMT, D, TM>;
+  using C = Cfg<DT, FMT, D, TM>;
   constexpr int bytes = 1024 + C::kOffCtl + (int)sizeof(Ctl<TM, C::kSlots>);
   static_assert(bytes <= 232448 && C::kOffCtl % 16 == 0, "shared memory");
   static std::atomic<bool> sized[64];

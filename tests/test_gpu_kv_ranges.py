@@ -155,3 +155,180 @@ def test_many_small_weights_beside_a_large_one(n, group, gap, sink, fmt):
     """As above for 16-bit caches and for many rows."""
     c, q, out, lse, scale = _one_key_above(6000, n, group, "f16", fmt, gap, sink, 40)
     _check(c, 0, q, out, lse, group, scale, once=n * group > 32)
+
+
+# ---------------------------------------------------------------------------
+# values of V that are not finite, and the largest ones
+
+
+def _set(c, b, part, pos, h, d, bits):
+    """The stored bits of one value (16-bit pattern or e4m3 code)."""
+    H, D, pt = c.H, c.D, c.pt
+    at = ((part * H + h) * pt + pos % pt) * D + d
+    pages = c.pool.pages.view(_torch().uint8 if c.fmt else _torch().int16).view(-1, c.pool.desc.page_elems * (2 if c.fmt else 1))
+    pages[int(c.table[b, pos // pt]), at] = bits if bits < 0x8000 else bits - 0x10000
+
+
+def _set_scale(c, b, part, pos, h, value):
+    H, D, pt = c.H, c.D, c.pt
+    pages = c.pool.pages.view(_torch().float32).view(-1, c.pool.desc.page_elems // 2)
+    pages[int(c.table[b, pos // pt]), 2 * H * pt * D // 4 + (part * H + h) * pt + pos % pt] = value
+
+
+def _odd_bits(c):
+    """Bits of infinity, -infinity and NaN (the only one there is in e4m3)."""
+    return (0x7f, 0xff, 0x7f) if c.fmt else (0x7f80, 0xff80, 0x7fc0) if c.dtype == "bf16" else (0x7c00, 0xfc00, 0x7e01)
+
+
+@pytest.mark.parametrize("window", [0, 40, 900])
+@pytest.mark.parametrize("dtype,fmt,D", [("bf16", 0, 64), ("f16", 0, 128), ("bf16", 1, 128), ("f16", 1, 64)])
+@pytest.mark.parametrize("n,group", [(1, 2), (2, 3), (5, 2), (7, 6), (40, 2), (300, 1), (150, 4)])
+def test_infinities_and_nan_among_the_values(n, group, dtype, fmt, D, window):
+    """Seen by all rows, by some and by none of an item, of one and of both signs, in items that are cut and not:
+    each output is what the definition makes of the keys that its row sees."""
+    H, L = 3, n + 1100
+    c = Cache([(n, L), (n, n), (n, L)], H, D, dtype, fmt, 16384, seed=n)
+    c.fill()
+    inf, ninf, nan = _odd_bits(c)
+    first = L - n
+    odd = [(5, 1, inf), (first - 700, 2, inf), (first - 60, 2, ninf), (first - 41, 3, inf), (first - 39, 4, nan),
+           (first, 5, ninf), (first + n // 2, 6, inf), (L - 1, 7, nan), (L - 1, 6, ninf), (first + n // 3, 8, inf),
+           (first - 900 + n // 2, 9, inf), (first - 40 + n // 2, 10, ninf)]
+    for h in (0, 2):
+        for pos, d, bits in odd:
+            if pos < L:
+                _set(c, 0, 1, pos, h, d + h, bits)
+        _set(c, 1, 1, n - 1, h, 20, inf)
+        _set(c, 1, 1, n // 2, h, 21, ninf)
+    if fmt:  # whole rows: infinite and NaN scales, seen by some
+        _set_scale(c, 1, 1, n // 2, 1, math.inf)
+        _set_scale(c, 2, 1, first + n // 2, 1, math.nan)
+        _set_scale(c, 2, 1, L - 1, 0, -math.inf)
+        _set_scale(c, 2, 1, first - 39, 2, math.inf)
+    rng = np.random.default_rng(3)
+    q = R.from_bits(R.to_bits(rng.standard_normal((c.T, H * group, D)), dtype), dtype)
+    out, lse = _attend(c, _dev(q.reshape(c.T, -1), dtype), H * group, window=window)
+    assert c.check()[0] == 0
+    scale = 1 / math.sqrt(D)
+    got = R.from_bits(_host(out), dtype).reshape(-1, H * group, D)
+    gl = lse.double().cpu().numpy()
+    for b in range(3):
+        rows = slice(b * n, b * n + n)
+        K, V = c.rows(b, 0), c.rows(b, 1)
+        Lb = c.lens[b][1]
+        with np.errstate(invalid="ignore"):
+            want, wl, _, _ = R.attention(q[rows], K, V, Lb - n, scale, window)
+        g = got[rows]
+        assert np.array_equal(np.isnan(g), np.isnan(want)), (b, np.argwhere(np.isnan(g) != np.isnan(want))[:6])
+        assert np.array_equal(np.isinf(g), np.isinf(want)) and np.array_equal(g[np.isinf(g)], want[np.isinf(want)]), b
+        # and where it is finite, the values: V's others with these at zero
+        V = np.where(np.isfinite(V), V, 0)
+        want, wl, A, S = R.attention(q[rows], K, V, Lb - n, scale, window)
+        p = 2.0 ** -11 if fmt else U[dtype] if n * group > 32 else 2.0 ** -16
+        tol = U[dtype] * np.abs(want) + A * (2 * ((D + 6) * 2.0 ** -23 * S[..., None] + 2.0 ** -21) + p + 2 * (Lb + 8) * 2.0 ** -23)
+        tol = tol + Lb * 2.0 ** -27 * np.abs(V).max(initial=0) + 2.0 ** -24
+        if fmt and dtype == "bf16":
+            tol = tol + A * (2 * D * 2.0 ** -24 * np.abs(q).max() * np.abs(K).max() * scale)
+        fin = np.isfinite(g)
+        assert np.all(np.abs(g - want)[fin] <= tol[fin]), b
+        assert np.all(np.abs(gl[rows] - wl) <= 2.0 ** -13 * (1 + np.abs(wl))), b
+
+
+def _long(n, group, fmt, L=9000, H=4, D=128):
+    """A long sequence beside a short one, filled on the device."""
+    torch = _torch()
+    c = Cache([(n, L), (1, 700)], H, D, "bf16", fmt, 32768)
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    if fmt:
+        by = c.pool.pages.view(torch.uint8)
+        by.copy_(torch.randint(0, 0x70, by.shape, dtype=torch.uint8, generator=gen, device="cuda"))
+        by.bitwise_or_(torch.randint(0, 2, by.shape, dtype=torch.uint8, generator=gen, device="cuda") * 128)
+        m = 2 * H * c.pt * D // 4
+        c.pool.pages.view(torch.float32).view(-1, c.pool.desc.page_elems // 2)[:, m:m + 2 * H * c.pt].fill_(0.01)
+    else:
+        c.pool.pages.normal_(generator=gen)
+    q = torch.randn(c.T, H * group * D, generator=gen, device="cuda").to(torch.bfloat16)
+    return c, q
+
+
+@pytest.mark.parametrize("where", ["seen by all", "newer"])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("n,group", [(1024, 8), (5, 8), (2, 4)])
+def test_values_that_are_not_finite_change_nothing_else_and_take_little_time(n, group, fmt, where):
+    torch = _torch()
+    c, q = _long(n, group, fmt)
+    H, D, hq = c.H, c.D, c.H * group
+    L = c.lens[0][1]
+    # one early key, or the newest one and others in between, so that items have keys that most rows do not see
+    keys = [100] if where == "seen by all" else list(range(L - n + 31, L, 32)) + [L - 1]
+    for pos in keys:
+        for h in range(H):
+            _set(c, 0, 1, pos, h, 3, 0)
+    ws = torch.empty(G.slora_kv_attention_workspace_bytes(c.pool.h, c.layout, hq, 2, c.T, n), dtype=torch.uint8, device="cuda")
+    lse = torch.empty(c.T, hq, device="cuda")
+
+    def timed():
+        ms = []
+        out = torch.empty_like(q)
+        for _ in range(5):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            _attend(c, q, hq, out=out, lse=lse, ws=ws, stream=torch.cuda.current_stream())
+            e[1].record()
+            torch.cuda.synchronize()
+            ms.append(e[0].elapsed_time(e[1]))
+        assert c.check()[0] == 0
+        return out.view(-1, hq, D), sorted(ms)[2]
+
+    ref, t0 = timed()
+    for pos in keys:
+        for h in range(H):
+            _set(c, 0, 1, pos, h, 3, _odd_bits(c)[0])
+    got, t1 = timed()
+    sees = torch.arange(n, device="cuda") + L - n >= keys[0]
+    odd = got[:n, :, 3].float()
+    assert bool((torch.isnan(odd) if fmt else odd == math.inf)[sees].all())
+    same = got.view(torch.int16) == ref.view(torch.int16)
+    same[:n, :, 3] |= sees[:, None]
+    assert bool(same.all())
+    assert t1 <= 4 * t0 + 1.0, (t0, t1)
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", 0), ("f16", 0), ("bf16", 1), ("f16", 1)])
+@pytest.mark.parametrize("n,group", [(1, 2), (5, 3), (5, 8), (40, 2), (300, 2)])
+def test_the_largest_values(n, group, dtype, fmt):
+    """V at the end of the type's range, one sign and equal: the mean is that value, in items that are cut and not."""
+    torch = _torch()
+    H, D = 2, 64
+    top = 65504.0 if dtype == "f16" else R.from_bits(np.array([0x7f7f], np.uint16), "bf16")[0]
+    lens = [(n, n + 3000), (n, n), (1, 60)]
+    c = Cache(lens, H, D, dtype, fmt, 8192, seed=n)
+
+    def spoil(b, part, x):
+        if part:
+            x[:] = top
+    c.fill(spoil=spoil)
+    q = R.from_bits(R.to_bits(np.random.default_rng(3).standard_normal((c.T, H * group, D)) * 3, dtype), dtype)
+    out, lse = _attend(c, _dev(q.reshape(c.T, -1), dtype), H * group)
+    assert c.check()[0] == 0 and torch.isfinite(lse).all()
+    got = R.from_bits(_host(out), dtype)
+    # rounding to the type may pass its end where the sums' errors do: half a step there, and no more
+    p = 2.0 ** -11 if fmt else U[dtype] if n * group > 32 else 2.0 ** -16
+    near = np.abs(got - top) <= top * (U[dtype] + p + 2 * 3100 * 2.0 ** -23)
+    assert np.all(near | (got == np.inf))
+    # half of it and a quarter: no way past the end
+    c2 = Cache(lens, H, D, dtype, fmt, 8192, seed=n)
+
+    def half(b, part, x):
+        if part:
+            x[:] = top / 2 * np.where(np.arange(len(x)) % 2, 1.0, 0.5)[:, None, None]
+    c2.fill(spoil=half)
+    out, lse = _attend(c2, _dev(q.reshape(c2.T, -1), dtype), H * group)
+    got = R.from_bits(_host(out), dtype).reshape(-1, H * group, D)
+    at = 0
+    for b, (m, L) in enumerate(lens):
+        want, _, _, _ = R.attention(q[at:at + m], c2.rows(b, 0), c2.rows(b, 1) / top, L - m, 1 / math.sqrt(D), 0)
+        S = 3 * 9 * math.sqrt(D)  # |q| |k| D / sqrt(D), of values of 3 sigma
+        tol = U[dtype] + p + 2 * ((D + 6) * 2.0 ** -23 * S + 2.0 ** -21) + 2 * (L + 8) * 2.0 ** -23 + D * 2.0 ** -22 * S / 8
+        assert np.all(np.abs(got[at:at + m] / top - want) <= tol), (b, np.abs(got[at:at + m] / top - want).max(), tol)
+        at += m
