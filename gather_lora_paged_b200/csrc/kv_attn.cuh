@@ -205,7 +205,7 @@ struct Item {
   int flags;              // 1: it starts here, 2: it ends here, 4: the run's last
   int odd;                // a V row that some rows see and others do not held values that are not finite
   int shut, late;         // keys above `shut`, or at `late` and below, are not seen by all rows
-  int pad[2];
+  int open0, open1;       // which need no looking at: of this run's tiles, those in [open0, open1)
 };
 
 constexpr int kNever = -(1 << 30);  // below every position, and that less a position is a number
@@ -228,7 +228,9 @@ __device__ __forceinline__ Item item_of(const KvAttnDev& A, const Cursor<TM, TK,
   x.odd = 0;
   x.shut = x.first + token_of(A, x.rt * TM);
   x.late = A.window > 0 ? x.first + token_of(A, x.rt * TM + x.R - 1) - A.window : kNever;
-  x.pad[0] = x.pad[1] = 0;
+  x.open0 = (x.late >> 7) + 1 - x.tile;
+  x.open1 = x.hi - 1 <= x.shut ? INT32_MAX : ((x.shut + 1) >> 7) - x.tile;
+  static_assert(TK == 128, "the shifts");
   return x;
 }
 
@@ -270,7 +272,6 @@ template <bool CODES, int DT, int NC, typename At>
 __device__ __forceinline__ void clean_tile(Item* x, int key0, const float* scales, At at) {
   const int lane = threadIdx.x & 31, shut = x->shut - key0, late = x->late - key0;
   const int first = max(x->lo - key0, 0), end = min(x->hi - key0, kKvTile);
-  if (end - 1 <= shut && first > late) return;
   bool odd = false;
 #pragma unroll 1
   for (int k = first + lane; k < end; k += 32) {

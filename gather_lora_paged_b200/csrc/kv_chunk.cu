@@ -29,10 +29,10 @@
 // has met is 2^7..2^8 units where the unit is set, and 2^15 at most before it moves.
 //
 // What bounds it: both products of a tile take 2100 cycles (128 columns and 16 elements 64), the
-// exponentials of its 256 x 128 weights as long on the special-function units; a tile takes 3300, as
+// exponentials of its 256 x 128 weights as long on the special-function units; a tile takes 3400, as
 // a q tile's softmax (2200) and its products (1050) follow one another.  2 x 1024..2048 tokens over 8192 keys, 64
-// heads on 8 of 128, bf16: 1.05 to 1.18 ms, 1000 to 1100 TFLOP/s at 1.5 to 1.64 GHz (the power limit), tensor
-// pipe 60 % of the cycles.  A quarter of the exponentials as polynomials on the FMA pipe did not pay (1234 us for 1184):
+// heads on 8 of 128, bf16, three inputs in turn: 1.17 to 1.25 ms, 945 to 1010 TFLOP/s at 1.5 to 1.64 GHz (the power
+// limit), tensor pipe 60 % of the cycles.  A quarter of the exponentials as polynomials on the FMA pipe did not pay (1234 us for 1184):
 // the softmax waits for latencies and issue slots more than for the special-function units.
 #include <math.h>
 
@@ -60,8 +60,8 @@ constexpr float kMost = 0x1p15f;
 template <int FMT, int D>
 struct Cfg {
   // Keys of one S, the softmax's step.  With 64, S of the next tile's half is computed while the softmax is at
-  // the other half, but an MMA of N = 64 takes 55 cycles, of N = 128 69: 16-bit chunks over 8192 take 1249 us
-  // with 64 and 1145 with 128; in e4m3, where the softmax has more to do, a mixed step takes 122 and 145.
+  // the other half, but an MMA of N = 64 takes 55 cycles, of N = 128 69: 16-bit chunks over 8192 take 1300 us
+  // with 64 and 1207 with 128; in e4m3, where the softmax has more to do, a mixed step takes 129 and 138.
   static constexpr int kPart = FMT == SLORA_KV_16 ? 128 : 64;
   static constexpr int kPanel = 128 * 128;                 // 128 rows of 64 16-bit elements
   static constexpr int kSlot = D / 64 * kPanel;            // K or V of a tile
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
         const Item& x = item_at(it);
-        const int n_tiles = x.n_tiles, last = x.flags & 4, q_tiles = x.R > 128 ? 2 : 1;
+        const int n_tiles = x.n_tiles, last = x.flags & 4, q_tiles = x.R > 128 ? 2 : 1, open0 = x.open0, open1 = x.open1;
         if (n_tiles == 0) break;
         wait(&ctl->q_full, it & 1);
         wait(&ctl->kv_full[g % S], (g / S) & 1);
@@ -274,9 +274,10 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           const bool more = n + 1 < n_tiles;
           const uint32_t v = (g + 1) % S, k = (g + 2) % S;
           wait(&ctl->kv_full[v], ((g + 1) / S) & 1);
-          clean_tile<false, MT, D / 8>(&ctl->item[it % kItems], (x.tile + n) * kTK,
-                                       F8 ? scales + (((g >> 1) % kMeta) * 2 + 1) * kTK : nullptr,
-                                       [&](int k, int c) { return sb + C::kOffRing + v * C::kSlot + place(k, c); });
+          if (n < open0 || n >= open1)
+            clean_tile<false, MT, D / 8>(&ctl->item[it % kItems], (x.tile + n) * kTK,
+                                         F8 ? scales + (((g >> 1) % kMeta) * 2 + 1) * kTK : nullptr,
+                                         [&](int k, int c) { return sb + C::kOffRing + v * C::kSlot + place(k, c); });
           if (more) wait(&ctl->kv_full[k], ((g + 2) / S) & 1);
 #pragma unroll 1
           for (int step = 0; step < 2 * q_tiles; ++step) {  // in the order in which the weights come
@@ -478,16 +479,21 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
 #pragma unroll 1
     for (uint32_t it = 0;; ++it) {
       const Item& x = item_at(it);
-      const int n_tiles = x.n_tiles, tile0 = x.tile, R = x.R, flags = x.flags, first = x.first, r_item = x.rt * kTM;
+      const int n_tiles = x.n_tiles;
       const bool none = over() || n_tiles == 0;
       if (wg == 0 ? any_of<1, 128>(none) : any_of<2, 128>(none)) break;
-      if (wg == 0 || R > 128) {
+      if (wg == 0 || x.R > 128) {
         const int r = wg * 128 + (warp & 3) * 32 + lane;
-        const int t = r < R ? token_of(A, r_item + r) : 0;
-        const int pos = r < R ? first + t : -1;
-        const int low = A.window > 0 && r < R ? pos - A.window : -1;   // keys above it are seen
-        const int pmin = first + token_of(A, r_item + wg * 128);       // of the first row of this q tile
-        const int pmax = first + token_of(A, r_item + R - 1);
+        int pos = -1, low = -1, pmin, pmax;  // of this row (keys above `low` are seen), of this q tile's first, the item's last
+        {
+          const int R = x.R, first = x.first, r_item = x.rt * kTM;
+          if (r < R) {
+            pos = first + token_of(A, r_item + r);
+            if (A.window > 0) low = pos - A.window;
+          }
+          pmin = first + token_of(A, r_item + wg * 128);
+          pmax = first + token_of(A, r_item + R - 1);
+        }
         float m = -INFINITY, l = 0.f, cr = A.c;
         float unit = -126.f, inv_unit = 0x1p126f;  // e4m3: log2 of the unit of this row's weights
         if (F8) {
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
           wait(&ctl->s_full[wg][0], sn & 1);
           wait(&ctl->kv_full[g % S], (g / S) & 1);
           const float* const ks = scales + (ti % kMeta) * 2 * kTK;
-          const int key0 = (tile0 + n) * kTK;
+          const int key0 = (x.tile + n) * kTK;
           const uint4 have = *reinterpret_cast<const uint4*>(ctl->mask[ti % kMeta]);
           const bool masked = key0 + kTK - 1 > pmin || (A.window > 0 && key0 <= pmax - A.window) ||
                               (have.x & have.y & have.z & have.w) != FULL_MASK;
@@ -548,7 +554,20 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
               }
             }
             float mn = fmaxf(m, fmaf(fmaxf(max3(top[0], top[1], top[2]), top[3]), cr, -(float)kLift));
-            float f = 1.f;  // what scales the products so far
+            auto scale_products = [&](float f) {  // those so far
+              wait(&ctl->pv_done[wg], (pv + 1) & 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 32) {
+                float o[32];
+                ld32(to + i, o);
+                wait_ld32(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= f;
+                st32(to + i, o);
+              }
+            };
+            float f = 1.f;  // e4m3: what scales them
             if (__any_sync(FULL_MASK, mn > m + kSlack)) {
               // e4m3: a whole number, so that a reference moves beside the unit without a rounding of either
               if (F8) mn = ceilf(mn);
@@ -559,9 +578,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
                 f = unit == keep || m == -INFINITY ? 1.f : ex2(keep - unit);
                 inv_unit = __int_as_float((127 - (int)unit) << 23);
               }
-              if (!F8) f = a;
               m = mn;
               l *= a;
+              if (!F8 && (n > 0 || part > 0)) scale_products(a);
             }
             const float mz = m == -INFINITY ? 0.f : m;
             const uint64_t c2 = pair(cr, cr), m2 = pair(-mz, -mz);
@@ -596,19 +615,7 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
                 inv_unit = __int_as_float((127 - (int)unit) << 23);
               }
             }
-            if ((n > 0 || part > 0) && __any_sync(FULL_MASK, f != 1.f)) {
-              wait(&ctl->pv_done[wg], (pv + 1) & 1);  // the products so far
-              tc_fence_after();
-#pragma unroll 1
-              for (int i = 0; i < D; i += 32) {
-                float o[32];
-                ld32(to + i, o);
-                wait_ld32(o);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= f;
-                st32(to + i, o);
-              }
-            }
+            if (F8 && (n > 0 || part > 0) && __any_sync(FULL_MASK, f != 1.f)) scale_products(f);
             const uint64_t iu2 = pair(inv_unit, inv_unit);
 #pragma unroll
             for (int i = 0; i < kPart; i += 32) {  // the weights
@@ -643,9 +650,11 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
         // ---- the rows of this item, or their partials
         wait(&ctl->o_full[wg], on++ & 1);
         tc_fence_after();
-        const bool complete = (flags & 3) == 3;
-        const int hq0 = x.h * A.G, hq = r < R ? hq0 + (r_item + r) - t * A.G : 0;
-        const int64_t row0 = x.row0, tok = row0 + t;
+        // (the entry is read again: what the tiles do not need is not kept through them)
+        const bool complete = (x.flags & 3) == 3;
+        const int R = x.R, r_item = x.rt * kTM, t = r < R ? token_of(A, r_item + r) : 0;
+        const int hq = r < R ? x.h * A.G + (r_item + r) - t * A.G : 0;
+        const int64_t tok = x.row0 + t;
         const float inv = inverse(l);
         uint16_t* const orow = A.out + tok * A.ldo + (int64_t)hq * D;
         float* const part = parts + (size_t)(2 * blockIdx.x + (it > 0 ? 1 : 0)) * slot_floats(kTM, D);
@@ -696,11 +705,12 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_chunk(const __grid_constant__ KvA
       } else {
         ti += n_tiles;
       }
+      const int last = x.flags & 4;
       // all four warps are through with the entry
       if (wg == 0) sync_of<1, 128>();
       else sync_of<2, 128>();
       if ((tid & 127) == 0) arrive(&ctl->item_empty[it % kItems]);
-      if (flags & 4) break;
+      if (last) break;
     }
   }
   tc_fence_before();

@@ -41,9 +41,10 @@
 //         what is lost of a weight is under 2^-11 of it or 2^-28 of the row's largest with V's scales.
 //
 // Measured (three inputs in turn): 256 tokens of 32 heads (one row a kv head) over 200..2000 keys, 3.24 GB in
-// fp16: 507 us, 6.4 TB/s; one token, 64 heads on 8, over 130001 keys, bf16: 91 us, 5.8 TB/s (85 in this kernel, at
-// 6.2); 64 tokens, 64 heads on 8, over 1000..16000 keys in e4m3, 0.7 GB: 145 us, 4.8 TB/s: at 8 rows the
-// copies' issue, the softmax and HBM take about 1370 cycles each for a tile; with 40 rows the softmax takes 4000.
+// fp16: 500 to 509 us, 6.4 TB/s; one token, 64 heads on 8, over 130001 keys, bf16: 91 us, 5.8 TB/s (85 in this kernel, at
+// 6.2); 64 tokens, 64 heads on 8, over 1000..16000 keys in e4m3, 0.7 GB: 141 us, 5.0 TB/s: at 8 rows the
+// copies' issue, the softmax and HBM take about 1370 cycles each for a tile; with 40 rows (5 tokens each: 290 us) the
+// softmax takes 3700.
 // The copies go at 7.0 TB/s by themselves (16-byte cp.async, four warps); TMA's row gather brings 1.9, a bulk copy
 // per 1 KB 3.6.
 //
@@ -61,7 +62,7 @@ constexpr int kTK = kKvTile;   // keys per tile
 constexpr int kMinRun = 1;     // tiles that are worth a CTA of their own
 constexpr int kMeta = 8;       // tiles whose scales and masks are kept: what the ring holds, at least
 constexpr int kItems = 16;     // items that are known ahead
-constexpr float kNoRef = 0x1.fffffep127f;  // (negated) reference of a row that has seen no key
+constexpr float kNoRef = 0x1.fffffep127f;  // (negated) reference of a row that has seen no key: scores are above -2^127
 
 // TM: rows per item.  N is a multiple of 16 rows (e4m3: three columns a row).
 template <int DT, int FMT, int D, int TM>
@@ -390,8 +391,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 13) {
       // ------------------------------------------------------ the run's items
-      // an item's lead.  0, 1, 2 tiles: 256 tokens (8 rows, 16-bit) 500, 488, 501 us, 64 tokens over an e4m3 cache 138,
-      // 130, 128; 2, 4 tiles: a mixed step with items of 40 rows 145, 142.
+      // an item's lead.  0, 1, 2 tiles: 256 tokens (8 rows, 16-bit) 500, 481, 495 us, 64 tokens over an e4m3 cache 130,
+      // 123, 124; 2, 3, 4 tiles: a mixed step with items of 40 rows 129, 129, 127.
       constexpr int E = TM <= 16 ? 1 : 3;
       Cursor<TM, kTK, E> c;
       Cut cut;
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
         uint32_t qslot = 0, qphase = 0, qit = 0, vslot = 1, vphase = 0, vit = 0, obuf = 0;
         int qleft = 0, vleft = 0, qn = 0, vn = 0, vkey = 0;
         int qlast = 0, vlast = 0;  // the item is the run's last
-        bool first = true, vborder = false;  // (it has keys that not all rows see)
+        int vt = 0, vn0 = 0, vn1 = 0;
+        bool first = true;
 #pragma unroll 1
         for (int step = 0;; ++step) {
           if (qleft > 0 || !qlast) {  // scores of tile `step`
@@ -549,7 +551,9 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               vleft = x.n_tiles;
               vlast = x.flags & 4;
               vkey = x.tile * kTK;
-              vborder = x.hi - 1 > x.shut || x.lo <= x.late;
+              vn0 = x.open0;
+              vn1 = x.open1;
+              vt = 0;
               if (__any_sync(FULL_MASK, over())) break;
               vn = !F8 ? (x.R + 7) / 8 * 2 : TM == 8 ? (x.R + 3) / 4 * 2 : (x.R + 7) / 8 * 4;
               first = true;
@@ -557,12 +561,12 @@ __global__ void __launch_bounds__(kNT, 1) k_kv_decode(const __grid_constant__ Kv
               wait(&ctl->o_empty[obuf], (((vit - 1) / C::kOBufs) & 1) ^ 1);
             }
             wait(&ctl->kv_full[vslot], vphase);
-            if (vborder)
+            if (vt < vn0 || vt >= vn1)
               clean_tile<F8, DT, C::kRow / 16>(
-                  &ctl->item[(vit - 1) % kItems], vkey,
+                  &ctl->item[(vit - 1) % kItems], vkey + vt * kTK,
                   F8 ? reinterpret_cast<const float*>(smem + C::kOffScale) + ((ti % kMeta) * 2 + 1) * kTK : nullptr,
                   [&](int k, int c) { return sb + vslot * C::kSlot + place<W>(kTK, k, c); });
-            vkey += kTK;
+            ++vt;
             wait(&ctl->p_full[ti & 1], (ti >> 1) & 1);
             fence_async_smem();
             tc_fence_after();
