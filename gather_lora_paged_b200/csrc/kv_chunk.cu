@@ -29,10 +29,10 @@
 // has met is 2^7..2^8 units where the unit is set, and 2^15 at most before it moves.
 //
 // What bounds it: both products of a tile take 2100 cycles (128 columns and 16 elements 64), the
-// exponentials of its 256 x 128 weights as long on the special-function units; a tile takes 3400, as
+// exponentials of its 256 x 128 weights as long on the special-function units; a tile takes 3300, as
 // a q tile's softmax (2200) and its products (1050) follow one another.  2 x 1024..2048 tokens over 8192 keys, 64
-// heads on 8 of 128, bf16, three inputs in turn: 1.17 to 1.25 ms, 945 to 1010 TFLOP/s at 1.5 to 1.64 GHz (the power
-// limit), tensor pipe 60 % of the cycles.  A quarter of the exponentials as polynomials on the FMA pipe did not pay (1234 us for 1184):
+// heads on 8 of 128, bf16, three inputs in turn: 1.18 ms, 1000 TFLOP/s at 1.5 to 1.64 GHz (the power
+// limit), tensor pipe 58 % of the cycles.  A quarter of the exponentials as polynomials on the FMA pipe did not pay (1234 us for 1184):
 // the softmax waits for latencies and issue slots more than for the special-function units.
 #include <math.h>
 

@@ -198,8 +198,9 @@ cudaError_t launch_kv_read(const KvDev& P, int dtype, int fmt, int D, void* k, i
 // Attention: kv_decode.cu takes the sequences of up to kv_stream_rows rows per kv head, kv_chunk.cu
 // those of more, then the join of the items that were cut.  One row tile of kv_decode.cu is as far as
 // it goes: a second one would read the cache again, and kv_chunk.cu's cost of a key hardly depends on
-// the rows.  48 sequences over 1000..8000 keys, 8 kv heads of 128, 16-bit: 32 rows 134 us here and 162
-// there, 40 rows 218 and 164; e4m3: 48 rows 276 and 334.
+// the rows.  48 sequences over 1000..8000 keys, 8 kv heads of 128, 16-bit: 16 rows 108 us here, 32 rows 113 here and
+// 161 there, 40 rows 162 there (and 122 with a row tile of 48, which has not been built in); e4m3: 32 rows 132 here,
+// 40 rows 158 and 298, 48 rows 172 and 300.
 constexpr int kv_stream_rows(int fmt) { return fmt == SLORA_KV_16 ? 32 : 48; }
 // Rows of its row tiles, as many as the call's largest sequence needs: the code for 8 rows is a
 // fraction of that for 48, and its ring of copies is deeper.

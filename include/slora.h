@@ -359,7 +359,8 @@ int32_t slora_kv_page_tokens(const slora_pool* pool, const slora_kv_layout_t* la
  * So one step's three arrays serve the write of its new tokens, their attention
  * and, with kv_len[b] the end of a range, the reading of any range.  Checked on
  * the device: a sequence whose rows or kv_len are out of range is skipped
- * (code 8, info = sequence); a position whose page id lies outside the pool is
+ * (code 8, info = sequence; where row_start does not ascend, also rows of other
+ * sequences may be left out); a position whose page id lies outside the pool is
  * not written or read, and attention leaves its key out (code 9, info =
  * sequence).  Page ids are not checked against ownership on the device: that is
  * slora_kv_check_batch.  Two sequences may share pages (a common prefix) as long
@@ -403,10 +404,15 @@ slora_status_t slora_kv_read(slora_pool* pool, const slora_kv_layout_t* layout, 
  * position and, if window > 0, j > position - window; lse[i, hq] = log sum_j w_j
  * (natural; T x n_q_heads fp32 contiguous; may be NULL).  A row that sees no key
  * gets 0 and -inf.  Keys that a row does not see have no influence on it,
- * whatever their bits.  q, out: T x n_q_heads*head_dim, not overlapping.  Sums and
+ * whatever their bits.  An infinity in a V row that it sees makes its output that
+ * infinity, a NaN or infinities of both signs a NaN.
+ * q, out: T x n_q_heads*head_dim, not overlapping.  Sums and
  * statistics are fp32, out is rounded once; the weights meet V as two 16-bit halves
  * each (a 16-bit cache and at most 32 rows, tokens times query heads of a kv head,
- * in the sequence), as one 16-bit value (more rows), or as their fp16 value (e4m3).
+ * in the sequence), as one 16-bit value (more rows), or, times V's scale and relative to the
+ * largest of these that the row has met, as their fp16 value (e4m3).  What falls below fp16's
+ * least step is under 2^-28 of the row's largest weight (fp16, e4m3).  An e4m3 cache takes
+ * q's elements relative to the row's largest, or to 2^-100 where that is less, and K below 2^120.
  *   - max_rows: a host-side bound on the rows of any one sequence (longer ones
  *     are skipped, code 8): 1 for a decode step, T where nothing is known;
  *   - workspace: slora_kv_attention_workspace_bytes() bytes of device memory,
