@@ -481,8 +481,13 @@ __device__ __forceinline__ void join_item(const KvAttnDev& A, const void* worksp
         for (int k = 0; k < kAhead; ++k) {
           const float wk = __shfl_sync(FULL_MASK, w, (j + k) & 31);
           if (j + k < n) {
+            if (wk != 0.f) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += wk * v[k][e];
+              for (int e = 0; e < E; ++e) o[e] += wk * v[k][e];
+            } else {  // no weight in fp32, but some: an infinity stays one
+#pragma unroll
+              for (int e = 0; e < E; ++e) o[e] += fabsf(v[k][e]) < INFINITY ? 0.f : v[k][e];
+            }
           }
         }
       }

@@ -234,6 +234,33 @@ def test_infinities_and_nan_among_the_values(n, group, dtype, fmt, D, window):
         assert np.all(np.abs(gl[rows] - wl) <= 2.0 ** -13 * (1 + np.abs(wl))), b
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,group", [(1, 2), (40, 2)])
+def test_an_infinity_among_keys_of_next_to_no_weight(n, group, dtype):
+    """The first half of a long cache is 75 nats below the rest (2^-108: parts of items that weigh nothing in fp32
+    beside the others), and holds infinities: they are what the definition makes of them all the same."""
+    H, D, L = 1, 64, 30000
+    c = Cache([(n, L)], H, D, dtype, 0, 65536, seed=n)
+
+    def spoil(b, part, x):
+        if not part:
+            x *= 0.1
+            x[:L // 2, :, 0] = -100.0
+            x[L // 2:, :, 0] = 0.0
+    c.fill(spoil=spoil)
+    inf, ninf, _ = _odd_bits(c)
+    for pos, d, bits in [(100, 1, inf), (7000, 2, ninf), (100, 3, inf), (9000, 3, ninf)]:
+        _set(c, 0, 1, pos, 0, d, bits)
+    q = np.random.default_rng(3).standard_normal((n, H * group, D))
+    q[:, :, 0] = 6.0
+    q = R.from_bits(R.to_bits(q, dtype), dtype)
+    out, _ = _attend(c, _dev(q.reshape(n, -1), dtype), H * group)
+    assert c.check()[0] == 0
+    got = R.from_bits(_host(out), dtype).reshape(n, H * group, D)
+    assert np.all(got[..., 1] == np.inf) and np.all(got[..., 2] == -np.inf) and np.isnan(got[..., 3]).all()
+    assert np.isfinite(np.delete(got, [1, 2, 3], -1)).all()
+
+
 def _long(n, group, fmt, L=9000, H=4, D=128):
     """A long sequence beside a short one, filled on the device."""
     torch = _torch()
