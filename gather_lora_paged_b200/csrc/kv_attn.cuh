@@ -277,7 +277,7 @@ __device__ __forceinline__ void clean_tile(Item* x, int key0, const float* scale
   for (int k = first + lane; k < end; k += 32) {
     if (k <= shut && k > late) continue;
     if (scales != nullptr) odd |= !(fabsf(scales[k]) < INFINITY);
-#pragma unroll 4
+#pragma unroll 1  // (four times the code takes 256 short e4m3 caches from 55 us to 58, though it never runs there)
     for (int c = 0; c < NC; ++c) {
       uint32_t w[4], f[4];
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at(k, c)) : "memory");

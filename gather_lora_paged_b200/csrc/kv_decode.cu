@@ -43,7 +43,7 @@
 // Measured (three inputs in turn): 256 tokens of 32 heads (one row a kv head) over 200..2000 keys, 3.24 GB in
 // fp16: 500 to 509 us, 6.4 TB/s; one token, 64 heads on 8, over 130001 keys, bf16: 91 us, 5.8 TB/s (85 in this kernel, at
 // 6.2); 64 tokens, 64 heads on 8, over 1000..16000 keys in e4m3, 0.7 GB: 141 us, 5.0 TB/s: at 8 rows the
-// copies' issue, the softmax and HBM take about 1370 cycles each for a tile; with 40 rows (5 tokens each: 290 us) the
+// copies' issue, the softmax and HBM take about 1370 cycles each for a tile; with 40 rows (5 tokens each: 286 us) the
 // softmax takes 3700.
 // The copies go at 7.0 TB/s by themselves (16-byte cp.async, four warps); TMA's row gather brings 1.9, a bulk copy
 // per 1 KB 3.6.
